@@ -14,6 +14,8 @@
  *        K_t = W_UK c_KV, V_t = W_UV c_KV.
  *   [IA] ia.com.br, "Como a MLA da DeepSeek cortou 93% da memoria ...", section
  *        "Um resumo no lugar de 128 copias": RoPE kept out of the compression as 64 numbers.
+ *   [MD] Medium mirror, "How Transformers Become Faster And Smarter: From KV Cache to MLA",
+ *        section "KV Cache": causal mask; the rows of past tokens never change.
  *
  * Conventions shared by every call
  *   - All pointers except `dims` are DEVICE pointers owned by the caller; the library never
@@ -293,6 +295,91 @@ int mla_append_absorb_fp8(const mla_dims* dims, const void* h, const void* w_dkv
 int mla_out_proj_fp8(const mla_dims* dims, const float* o_lat, const void* w_uv,
                      const void* w_o_codes, const float* w_o_scale, void* o_heads, void* out,
                      void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * Several new tokens per sequence: whole prompts, and chunks of new tokens over a cache that
+ * already holds a sequence's beginning ([MD] "KV Cache": the rows of past tokens do not change,
+ * so a prompt's rows can enter the cache in one go or in pieces, and every token sees the
+ * tokens up to itself).
+ *
+ * Packed batches.  The new tokens of all sequences lie one behind the other: sequence b's are
+ * tokens [cu_tokens[b], cu_tokens[b + 1]) of n_tokens, cu_tokens [batch + 1] int32 on the device,
+ * cu_tokens[0] = 0, not decreasing, cu_tokens[batch] <= n_tokens.  A sequence may have none.
+ * Tokens behind the last sequence are neither read nor written.  A cu_tokens that decreases or
+ * passes n_tokens raises MLA_STATUS_BAD_LENGTH and gives undefined results for the sequences it
+ * damages, without an access out of range.
+ * seq_lens[b] counts the sequence's rows with its new tokens: token i of n_b is row
+ * seq_lens[b] - n_b + i.  dims.batch is the number of sequences; in these calls it is not limited
+ * to 128, and d_model is not used.  n_tokens = 0 does nothing.
+ * Strides are in elements, at least the row they step over and at most 2^36, and multiples of 16
+ * bytes (else MLA_ERR_ARG), so a view of a wider tensor can be passed as it is.
+ *
+ * mla_append_rows -- the rows of the new tokens into the cache, the rotation applied on the way:
+ *   pool slot of row p = seq_lens[b] - n_b + i:  [c_kv[t] | R(p) k_r[t]],
+ *   k_rope[t] = R(p) k_r[t],   q_rope_out[t][h] = R(p) q_rope[t][h],
+ * R(p) the RoPE of the conventions above, in fp32 and rounded once.
+ *   c_kv [n_tokens, d_c], k_r [n_tokens, d_rope], rows c_kv_stride / k_r_stride apart.
+ *   k_rope   nullable: [n_tokens, d_rope] contiguous (for mla_prompt_attn).
+ *   q_rope, q_rope_out  nullable together: [n_tokens, H, d_rope]; q_rope_out may be q_rope (in
+ *            place), or the last d_rope columns of q_cat, but may not overlap it otherwise.
+ * A token whose row lies outside its sequence's pages (MLA_STATUS_BAD_POSITION) or whose page id
+ * is out of range (MLA_STATUS_BAD_PAGE) is skipped: nothing of it is written.  Two tokens may not
+ * share a slot.
+ */
+int mla_append_rows(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tokens,
+                    const int32_t* seq_lens, const void* c_kv, int64_t c_kv_stride,
+                    const void* k_r, int64_t k_r_stride, const int32_t* page_table,
+                    int32_t max_pages, void* cache_pool, int32_t num_pages, void* k_rope,
+                    const void* q_rope, int64_t q_token_stride, int64_t q_head_stride,
+                    void* q_rope_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                    mla_stream_t stream);
+
+/*
+ * mla_prompt_attn -- causal attention over whole prompts, in the form without absorption ([LP]
+ * "Classic attention ..."): for token i of a sequence and head h, with key head g = h / (H /
+ * n_kv_heads),
+ *   s_j = scale * (q[i][h][:d_nope] . k_nope[j][g] + q[i][h][d_nope:] . k_rope[j]),  j <= i,
+ *   o[i][h] = sum_j softmax(s)_j v[j][g],   lse[i][h] = log sum_j exp(s_j).
+ *   q      [n_tokens, H, d_nope + d_rope], its last d_rope columns rotated already;
+ *   k_nope [n_tokens, n_kv_heads, d_nope],  v [n_tokens, n_kv_heads, d_v];
+ *   k_rope [n_tokens, d_rope], rotated, shared by all heads;
+ *   o      [n_tokens, H, d_v] contiguous (dims.dtype);  lse [n_tokens, H] fp32, nullable.
+ *   n_kv_heads divides n_heads (MLA_ERR_ARG); n_heads itself for MLA's up-projected keys.
+ *   softmax_scale: 0 selects 1/sqrt(d_nope + d_rope).
+ * No workspace.  The rows of one sequence never depend on another's, nor on what lies behind the
+ * last one.
+ */
+int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
+                    const int32_t* cu_tokens, const void* q, int64_t q_token_stride,
+                    int64_t q_head_stride, const void* k_nope, int64_t k_token_stride,
+                    int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
+                    const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                    float softmax_scale, void* o, float* lse, mla_stream_t stream);
+
+/*
+ * mla_chunk_attn -- attention of the new tokens over the paged latent cache, which holds their
+ * own rows already (mla_append_rows first): mla_decode_attn with several tokens per sequence,
+ *   s_j = scale * <q_cat[t][h], row_j>,  j <= seq_lens[b] - n_b + i;   p = softmax(s);
+ *   o_lat[t][h] = sum_j p_j c_j,   lse[t][h] = log sum_j exp(s_j).
+ *   q_cat  [n_tokens, H, d_c + d_rope];  pool, page_table, seq_lens, num_splits (at most 65536,
+ *          0 = automatic) as in mla_decode_attn.
+ *   o_lat  [n_tokens, H, d_c] of type o_dtype: dims.dtype, or MLA_FP32 (for mla_out_proj and
+ *          mla_merge_partials); on the bf16 path the weights p are rounded to bf16 either way.
+ *   lse    [n_tokens, H] fp32, nullable.
+ * A token that sees no row (n_b > seq_lens[b]) gets o_lat = 0, lse = -inf.  Lengths outside
+ * [0, max_pages * page_size] are clamped and raise MLA_STATUS_BAD_LENGTH, page ids out of range
+ * read page 0 and raise MLA_STATUS_BAD_PAGE.
+ * The workspace (mla_chunk_workspace_size, for the same dims, n_tokens and num_splits or larger
+ * ones) is scratch: calls that share it must be ordered.
+ */
+size_t mla_chunk_workspace_size(const mla_dims* dims, int32_t n_tokens, int32_t num_splits);
+
+int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tokens,
+                   const void* q_cat, const void* cache_pool, int32_t num_pages,
+                   const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                   float softmax_scale, int32_t num_splits, void* workspace,
+                   size_t workspace_bytes, void* o_lat, int32_t o_dtype, float* lse,
+                   mla_stream_t stream);
 
 /*
  * Native decode step over a stack of layers, end to end from host memory.

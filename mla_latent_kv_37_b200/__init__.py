@@ -63,6 +63,7 @@ class mla_layer(ctypes.Structure):
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _SIGS = {
     "mla_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(mla_dims), _I]),
@@ -92,6 +93,13 @@ _SIGS = {
     "mla_append_absorb_folded": (ctypes.c_int, [ctypes.POINTER(mla_dims), _P, _P, _P, _P, _P,
                                                 _P, _I, _P, _I, _P, _P, _P, _SZ, _P]),
     "mla_out_proj_folded": (ctypes.c_int, [ctypes.POINTER(mla_dims), _P, _P, _P, _P, _SZ, _P]),
+    "mla_append_rows": (ctypes.c_int, [ctypes.POINTER(mla_dims), _I, _P, _P, _P, _L, _P, _L, _P, _I,
+                                       _P, _I, _P, _P, _L, _L, _P, _L, _L, _P]),
+    "mla_prompt_attn": (ctypes.c_int, [ctypes.POINTER(mla_dims), _I, _I, _P, _P, _L, _L, _P, _L, _L,
+                                       _P, _L, _P, _L, _L, ctypes.c_float, _P, _P, _P]),
+    "mla_chunk_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(mla_dims), _I, _I]),
+    "mla_chunk_attn": (ctypes.c_int, [ctypes.POINTER(mla_dims), _I, _P, _P, _P, _I, _P, _I, _P,
+                                      ctypes.c_float, _I, _P, _SZ, _P, _I, _P, _P]),
     "mla_get_status": (ctypes.c_int, [_P]),
     "mla_error_string": (ctypes.c_char_p, [ctypes.c_int]),
     "mla_error_detail": (ctypes.c_char_p, []),
@@ -158,6 +166,19 @@ def _need(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_table(t, d: mla_dims):
+    _need(t, "page_table", torch.int32)
+    if t.dim() != 2 or t.shape[0] != d.batch:
+        raise ValueError(f"page_table must have shape ({d.batch}, max_pages), got {tuple(t.shape)}")
+
+
+def _need_pool(t, d: mla_dims):
+    _need(t, "cache_pool", _elem(d))
+    if t.dim() != 3 or t.shape[1:] != (d.page_size, d.d_c + d.d_rope):
+        raise ValueError(f"cache_pool must have shape (num_pages, {d.page_size}, "
+                         f"{d.d_c + d.d_rope}), got {tuple(t.shape)}")
 
 
 def _elem(d: mla_dims):
@@ -288,6 +309,128 @@ def mla_out_proj(d: mla_dims, o_lat, w_uv, ws, w_o=None, o_heads=None, out=None,
     rc = lib().mla_out_proj(ctypes.byref(d), _ptr(o_lat), _ptr(w_uv), _ptr(w_o), _ptr(o_heads),
                             _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "mla_out_proj")
+
+
+# ---------------------------------------------------------------------------------------------
+# several new tokens per sequence
+# ---------------------------------------------------------------------------------------------
+def _need_view(t, name, dtype, shape):
+    """A CUDA tensor of this type and shape whose last dimension is contiguous; the strides of the
+    others are the library's to check."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                         f"{tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _strides(t):
+    """Strides of the leading dimensions.  Where a dimension has one element, torch's stride says
+    nothing: the distance that a contiguous tensor would have stands in."""
+    out, least = [], t.shape[-1]
+    for i in range(t.dim() - 2, -1, -1):
+        s = t.stride(i) if t.shape[i] > 1 else least
+        out.append(s)
+        least = max(least, s * t.shape[i])
+    return out[::-1]
+
+
+def _one_device(*tensors):
+    """All tensors on the current device, which is where the library launches."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+
+
+def mla_append_rows(d: mla_dims, c_kv, k_r, cu_tokens, seq_lens, page_table, cache_pool, k_rope=None,
+                    q_rope=None, q_rope_out=None, stream=None):
+    """The rows [c_kv | RoPE(k_r)] of several new tokens per sequence into the paged cache.
+
+    c_kv [T, 512] and k_r [T, 64] of the packed tokens, cu_tokens [batch + 1], seq_lens [batch]
+    (rows with the new tokens).  k_rope [T, 64] also receives the rotated keys; q_rope [T, H, 64]
+    (a view of the queries) is rotated into q_rope_out (itself, or a view of q_cat)."""
+    e, T = _elem(d), c_kv.shape[0]
+    _need_view(c_kv, "c_kv", e, (T, d.d_c))
+    _need_view(k_r, "k_r", e, (T, d.d_rope))
+    _need(cu_tokens, "cu_tokens", torch.int32, (d.batch + 1,))
+    _need(seq_lens, "seq_lens", torch.int32, (d.batch,))
+    _need_table(page_table, d)
+    _need_pool(cache_pool, d)
+    _need(k_rope, "k_rope", e, (T, d.d_rope))
+    if (q_rope is None) != (q_rope_out is None):
+        raise ValueError("q_rope and q_rope_out go together")
+    qs = qo = (0, 0)
+    if q_rope is not None:
+        _need_view(q_rope, "q_rope", e, (T, d.n_heads, d.d_rope))
+        _need_view(q_rope_out, "q_rope_out", e, (T, d.n_heads, d.d_rope))
+        qs, qo = _strides(q_rope), _strides(q_rope_out)
+    _one_device(c_kv, k_r, cu_tokens, seq_lens, page_table, cache_pool, k_rope, q_rope, q_rope_out)
+    rc = lib().mla_append_rows(
+        ctypes.byref(d), T, _ptr(cu_tokens), _ptr(seq_lens), _ptr(c_kv), _strides(c_kv)[0],
+        _ptr(k_r), _strides(k_r)[0], _ptr(page_table), page_table.shape[1], _ptr(cache_pool),
+        cache_pool.shape[0], _ptr(k_rope), _ptr(q_rope), qs[0], qs[1], _ptr(q_rope_out), qo[0],
+        qo[1], _stream(stream))
+    _check(rc, "mla_append_rows")
+
+
+def mla_prompt_attn(d: mla_dims, q, k_nope, k_rope, v, cu_tokens, o, lse=None,
+                    softmax_scale: float = 0.0, stream=None):
+    """Causal attention over whole packed prompts: q [T, H, 192] (rotated), k_nope [T, Hk, 128],
+    k_rope [T, 64] (rotated, shared by the heads), v [T, Hk, 128], Hk dividing H -> o [T, H, 128],
+    lse [T, H].  q, k_nope, k_rope and v may be views with strides of 16-byte multiples."""
+    e, T, H = _elem(d), q.shape[0], d.n_heads
+    Hk = k_nope.shape[1] if k_nope.dim() == 3 else 0
+    _need_view(q, "q", e, (T, H, d.d_nope + d.d_rope))
+    _need_view(k_nope, "k_nope", e, (T, Hk, d.d_nope))
+    _need_view(k_rope, "k_rope", e, (T, d.d_rope))
+    _need_view(v, "v", e, (T, Hk, d.d_v))
+    _need(cu_tokens, "cu_tokens", torch.int32, (d.batch + 1,))
+    _need(o, "o", e, (T, H, d.d_v))
+    _need(lse, "lse", torch.float32, (T, H))
+    _one_device(q, k_nope, k_rope, v, cu_tokens, o, lse)
+    qs, ks, vs = _strides(q), _strides(k_nope), _strides(v)
+    rc = lib().mla_prompt_attn(
+        ctypes.byref(d), T, Hk, _ptr(cu_tokens), _ptr(q), qs[0], qs[1], _ptr(k_nope), ks[0], ks[1],
+        _ptr(k_rope), _strides(k_rope)[0], _ptr(v), vs[0], vs[1], float(softmax_scale), _ptr(o),
+        _ptr(lse), _stream(stream))
+    _check(rc, "mla_prompt_attn")
+
+
+def mla_chunk_workspace_size(d: mla_dims, n_tokens: int, num_splits: int = 0) -> int:
+    return int(lib().mla_chunk_workspace_size(ctypes.byref(d), n_tokens, num_splits))
+
+
+def chunk_workspace(d: mla_dims, n_tokens: int, num_splits: int = 0, device="cuda") -> torch.Tensor:
+    n = mla_chunk_workspace_size(d, n_tokens, num_splits)
+    if n == 0:
+        raise MlaError(-2, "mla_chunk_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mla_chunk_attn(d: mla_dims, q_cat, cache_pool, page_table, cu_tokens, seq_lens, o_lat, ws,
+                   lse=None, softmax_scale: float = 0.0, num_splits: int = 0, stream=None):
+    """Attention of several new tokens per sequence over the paged latent cache, which holds their
+    own rows already: q_cat [T, H, 576] -> o_lat [T, H, 512] (the cache's type, or fp32 for
+    mla_out_proj), lse [T, H].  `ws` from chunk_workspace(d, T, num_splits)."""
+    e, T, H = _elem(d), q_cat.shape[0], d.n_heads
+    _need(q_cat, "q_cat", e, (T, H, d.d_c + d.d_rope))
+    _need_pool(cache_pool, d)
+    _need_table(page_table, d)
+    _need(cu_tokens, "cu_tokens", torch.int32, (d.batch + 1,))
+    _need(seq_lens, "seq_lens", torch.int32, (d.batch,))
+    _need(o_lat, "o_lat", None if o_lat.dtype == e else torch.float32, (T, H, d.d_c))
+    _need(lse, "lse", torch.float32, (T, H))
+    _need(ws, "workspace", torch.uint8)
+    _one_device(q_cat, cache_pool, page_table, cu_tokens, seq_lens, o_lat, lse, ws)
+    rc = lib().mla_chunk_attn(
+        ctypes.byref(d), T, _ptr(cu_tokens), _ptr(q_cat), _ptr(cache_pool), cache_pool.shape[0],
+        _ptr(page_table), page_table.shape[1], _ptr(seq_lens), float(softmax_scale),
+        int(num_splits), _ptr(ws), ws.numel(), _ptr(o_lat),
+        MLA_FP32 if o_lat.dtype == torch.float32 else MLA_BF16, _ptr(lse), _stream(stream))
+    _check(rc, "mla_chunk_attn")
 
 
 def layer_structs(d: mla_dims, layers):

@@ -9,7 +9,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmla_b200.so")
-SOURCES = [os.path.join(HERE, "csrc", "mla_api.cu"), os.path.join(HERE, "csrc", "step_host.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("mla_api.cu", "multi_token.cu", "step_host.cu")]
 DEPS = [os.path.join(HERE, "csrc", f) for f in sorted(os.listdir(os.path.join(HERE, "csrc")))] + [
     os.path.join(ROOT, "include", "mla.h")]
 
@@ -23,7 +23,7 @@ def nvcc() -> str:
 
 def command(out: str = LIB, extra=()) -> list[str]:
     return [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-            "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+            "-std=c++17", "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
             *extra, "-o", out, *SOURCES]
 
 

@@ -19,6 +19,7 @@
 #include "fold.cuh"
 #include "fp8.cuh"
 #include "gemm_streamk.cuh"
+#include "host_services.h"
 
 namespace mla {
 
@@ -60,7 +61,9 @@ constexpr size_t kSmemPerBlockMax = 232448;  // 227 KiB opt-in limit per CTA
 // ------------------------------------------------------------------------------------------
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int check_dims(const mla_dims* d) {
+// `one_token`: the calls that take one token per sequence, whose bf16 products put the batch on
+// the MMA's columns.
+int check_dims(const mla_dims* d, bool one_token = true) {
   if (!d) return MLA_ERR_NULL_ARG;
   if (d->d_c != kDc || d->d_rope != kDr || d->d_nope != kDn || d->d_v != kDv ||
       d->page_size != kPageN)
@@ -69,7 +72,7 @@ int check_dims(const mla_dims* d) {
   if (d->d_model <= 0 || d->d_model % 64) return MLA_ERR_DIMS;
   if (d->batch < 1) return MLA_ERR_DIMS;
   if (d->dtype != MLA_BF16 && d->dtype != MLA_FP32) return MLA_ERR_DIMS;
-  if (d->dtype == MLA_BF16 && d->batch > 128) return MLA_ERR_DIMS;  // 2B <= 256 MMA columns
+  if (one_token && d->dtype == MLA_BF16 && d->batch > 128) return MLA_ERR_DIMS;  // 2B <= 256 MMA columns
   if (!(d->rope_theta > 0.f) || !std::isfinite(d->rope_theta)) return MLA_ERR_DIMS;
   return MLA_OK;
 }
@@ -664,6 +667,24 @@ int enqueue_decode(const DevCtx* c, const mla_dims* dims, const void* q_cat, con
   return last_launch();
 }
 }  // namespace
+
+// Services for the library's other translation units (host_services.h).
+int host_device(HostDevice* out) {
+  DevCtx* c = nullptr;
+  const int rc = device_ctx(&c);
+  if (rc == MLA_OK) *out = {c->sms, c->status};
+  return rc;
+}
+int host_cuda_error(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+int host_launched(int kernels) { return last_launch(kernels); }
+bool host_pdl() { return pdl_enabled(); }
+uint64_t host_wait_ns() { return wait_limit_ns(); }
+int host_check_dims(const mla_dims* d) { return check_dims(d, false); }
+int host_encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank,
+                const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                CUtensorMapSwizzle sw) {
+  return encode(m, dt, base, rank, dims, strides_bytes, box, sw);
+}
 }  // namespace mla
 
 using namespace mla;

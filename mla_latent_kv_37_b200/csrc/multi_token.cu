@@ -1,0 +1,267 @@
+// C ABI of the calls with several new tokens per sequence (see include/mla.h): rows into the
+// paged cache, attention over whole packed prompts, attention of a chunk over the paged cache.
+// Host side: argument validation before any CUDA call, workspace layout, launches.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "attn_simt.cuh"
+#include "chunk_plan.cuh"
+#include "host_services.h"
+#include "rows.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kDc = 512, kDr = 64, kDn = 128, kDv = 128, kPageN = 64;
+constexpr int kMaxParts = 1 << 16;
+constexpr float kLog2e = 1.4426950408889634f;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t elem_size(const mla_dims* d) { return d->dtype == MLA_BF16 ? 2 : 4; }
+// A stride (elements) of 16-byte multiples that does not run backwards; `least` elements lie
+// between two neighbours.  Zero is the one exception: all of them are the same.
+bool stride_ok(int64_t stride, int64_t least, size_t elem) {
+  return stride >= least && stride < (int64_t{1} << 36) && stride * static_cast<int64_t>(elem) % 16 == 0;
+}
+
+float resolve_scale(float softmax_scale) {
+  return softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(kDn + kDr));
+}
+
+// Kernel attributes, once per device.
+int set_attributes() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return host_cuda_error(e, "cudaGetDevice");
+  if (dev < 0 || dev >= 64) return MLA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return MLA_OK;
+  if ((e = cudaFuncSetAttribute(simt::prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(simt::Layout<192, 128>::kBytes))) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(simt::chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(simt::Layout<576, 512>::kBytes))) != cudaSuccess)
+    return host_cuda_error(e, "cudaFuncSetAttribute");
+  done[dev] = true;
+  return MLA_OK;
+}
+
+// Workspace of mla_chunk_attn: plan, then the partial results of the parts.
+struct ChunkSpace {
+  size_t plan, part_o, part_lse, total;
+  int tile_rows, max_tiles, parts;
+};
+int chunk_tile_rows(const mla_dims* d) { return simt::kRows; }
+
+ChunkSpace chunk_space(const mla_dims* d, int n_tokens, int num_splits, int sms) {
+  ChunkSpace w{};
+  w.tile_rows = chunk_tile_rows(d);
+  w.parts = num_splits > 0 ? num_splits : sms;
+  const int64_t rows = static_cast<int64_t>(n_tokens) * d->n_heads;
+  w.max_tiles = static_cast<int>(rows / w.tile_rows + std::min<int64_t>(d->batch, n_tokens));
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return o;
+  };
+  w.plan = take(4 * chunk::Plan::words(d->batch, w.max_tiles, w.parts));
+  w.part_o = take(2ull * w.parts * w.tile_rows * kDc * 4);
+  w.part_lse = take(2ull * w.parts * w.tile_rows * 4);
+  w.total = off;
+  return w;
+}
+
+// rows x columns of a call in int32 units on the device, page ids and lengths likewise
+bool counts_ok(const mla_dims* d, int32_t n_tokens) {
+  return static_cast<int64_t>(n_tokens) * d->n_heads <= INT32_MAX && d->batch < INT32_MAX;
+}
+bool pages_ok(int32_t num_pages, int32_t max_pages) {
+  return num_pages >= 1 && max_pages >= 1 &&
+         static_cast<int64_t>(num_pages) * kPageN <= INT32_MAX &&
+         static_cast<int64_t>(max_pages) * kPageN <= INT32_MAX;
+}
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" {
+
+int mla_append_rows(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tokens,
+                    const int32_t* seq_lens, const void* c_kv, int64_t c_kv_stride,
+                    const void* k_r, int64_t k_r_stride, const int32_t* page_table,
+                    int32_t max_pages, void* cache_pool, int32_t num_pages, void* k_rope,
+                    const void* q_rope, int64_t q_token_stride, int64_t q_head_stride,
+                    void* q_rope_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                    mla_stream_t stream) {
+  int rc = host_check_dims(dims);
+  if (rc) return rc;
+  if (n_tokens < 0 || !pages_ok(num_pages, max_pages)) return MLA_ERR_ARG;
+  if (n_tokens == 0) return MLA_OK;
+  if (!counts_ok(dims, n_tokens)) return MLA_ERR_ARG;
+  if (!cu_tokens || !seq_lens || !c_kv || !k_r || !page_table || !cache_pool ||
+      !q_rope != !q_rope_out)
+    return MLA_ERR_NULL_ARG;
+  const size_t e = elem_size(dims);
+  if (!stride_ok(c_kv_stride, kDc, e) || !stride_ok(k_r_stride, kDr, e)) return MLA_ERR_ARG;
+  if (q_rope && (!stride_ok(q_token_stride, kDr, e) || !stride_ok(q_head_stride, kDr, e) ||
+                 !stride_ok(q_out_token_stride, kDr, e) || !stride_ok(q_out_head_stride, kDr, e)))
+    return MLA_ERR_ARG;
+  if (!aligned(cu_tokens, 4) || !aligned(seq_lens, 4) || !aligned(page_table, 4) ||
+      !aligned(c_kv, 16) || !aligned(k_r, 16) || !aligned(cache_pool, 16) ||
+      !aligned(k_rope, 16) || !aligned(q_rope, 16) || !aligned(q_rope_out, 16))
+    return MLA_ERR_ALIGN;
+  HostDevice dev;
+  if ((rc = host_device(&dev))) return rc;
+  rows::Params p{};
+  p.n_tokens = n_tokens;
+  p.batch = dims->batch;
+  p.n_heads = dims->n_heads;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.cu = cu_tokens;
+  p.seq_lens = seq_lens;
+  p.page_table = page_table;
+  p.c_kv = c_kv;
+  p.k_r = k_r;
+  p.q = q_rope;
+  p.pool = cache_pool;
+  p.k_rope = k_rope;
+  p.q_out = q_rope_out;
+  p.c_stride = c_kv_stride;
+  p.kr_stride = k_r_stride;
+  p.q_tok = q_token_stride;
+  p.q_head = q_head_stride;
+  p.qo_tok = q_out_token_stride;
+  p.qo_head = q_out_head_stride;
+  p.theta = dims->rope_theta;
+  p.status = dev.status;
+  p.heads_per_block = 16;
+  const unsigned blocks = (static_cast<unsigned>(n_tokens) + rows::kTokens - 1) / rows::kTokens;
+  const unsigned slices =
+      q_rope ? (dims->n_heads + p.heads_per_block - 1) / p.heads_per_block : 0;
+  host_launch(dims->dtype == MLA_BF16 ? rows::append_rows_kernel<__nv_bfloat16>
+                                      : rows::append_rows_kernel<float>,
+              dim3(blocks, 1 + slices), dim3(rows::kThreads), 0,
+              reinterpret_cast<cudaStream_t>(stream), p);
+  return host_launched();
+}
+
+int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
+                    const int32_t* cu_tokens, const void* q, int64_t q_token_stride,
+                    int64_t q_head_stride, const void* k_nope, int64_t k_token_stride,
+                    int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
+                    const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                    float softmax_scale, void* o, float* lse, mla_stream_t stream) {
+  int rc = host_check_dims(dims);
+  if (rc) return rc;
+  if (n_tokens < 0 || n_kv_heads < 1 || dims->n_heads % n_kv_heads) return MLA_ERR_ARG;
+  if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale)) return MLA_ERR_ARG;
+  if (n_tokens == 0) return MLA_OK;
+  if (!counts_ok(dims, n_tokens)) return MLA_ERR_ARG;
+  if (!cu_tokens || !q || !k_nope || !k_rope || !v || !o) return MLA_ERR_NULL_ARG;
+  const size_t e = elem_size(dims);
+  if (!stride_ok(q_token_stride, kDn + kDr, e) || !stride_ok(q_head_stride, kDn + kDr, e) ||
+      !stride_ok(k_token_stride, kDn, e) || !stride_ok(k_head_stride, kDn, e) ||
+      !stride_ok(k_rope_stride, kDr, e) || !stride_ok(v_token_stride, kDv, e) ||
+      !stride_ok(v_head_stride, kDv, e))
+    return MLA_ERR_ARG;
+  if (!aligned(cu_tokens, 4) || !aligned(q, 16) || !aligned(k_nope, 16) || !aligned(k_rope, 16) ||
+      !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4))
+    return MLA_ERR_ALIGN;
+  HostDevice dev;
+  if ((rc = host_device(&dev)) || (rc = set_attributes())) return rc;
+  simt::PromptParams p{};
+  p.n_tokens = n_tokens;
+  p.batch = dims->batch;
+  p.n_heads = dims->n_heads;
+  p.n_kv_heads = n_kv_heads;
+  p.cu = cu_tokens;
+  p.q = q;
+  p.k_nope = k_nope;
+  p.k_rope = k_rope;
+  p.v = v;
+  p.q_tok = q_token_stride;
+  p.q_head = q_head_stride;
+  p.k_tok = k_token_stride;
+  p.k_head = k_head_stride;
+  p.kr_tok = k_rope_stride;
+  p.v_tok = v_token_stride;
+  p.v_head = v_head_stride;
+  p.scale_log2 = resolve_scale(softmax_scale) * kLog2e;
+  p.o = o;
+  p.lse = lse;
+  p.status = dev.status;
+  if (dims->dtype == MLA_BF16) return MLA_ERR_DIMS;
+  // every sequence has at most one tile that is not full
+  const unsigned tiles =
+      static_cast<unsigned>(n_tokens / simt::kRows + std::min(dims->batch, n_tokens));
+  host_launch(simt::prompt_kernel, dim3(tiles, dims->n_heads), dim3(simt::kThreads),
+              simt::Layout<192, 128>::kBytes, reinterpret_cast<cudaStream_t>(stream), p);
+  return host_launched();
+}
+
+size_t mla_chunk_workspace_size(const mla_dims* dims, int32_t n_tokens, int32_t num_splits) {
+  if (host_check_dims(dims) != MLA_OK || n_tokens < 0 || num_splits < 0 ||
+      num_splits > kMaxParts || !counts_ok(dims, n_tokens))
+    return 0;
+  HostDevice dev{148, nullptr};
+  (void)host_device(&dev);
+  return chunk_space(dims, n_tokens, num_splits, dev.sms).total;
+}
+
+int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tokens,
+                   const void* q_cat, const void* cache_pool, int32_t num_pages,
+                   const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                   float softmax_scale, int32_t num_splits, void* workspace,
+                   size_t workspace_bytes, void* o_lat, int32_t o_dtype, float* lse,
+                   mla_stream_t stream) {
+  int rc = host_check_dims(dims);
+  if (rc) return rc;
+  if (n_tokens < 0 || !pages_ok(num_pages, max_pages) || num_splits < 0 || num_splits > kMaxParts)
+    return MLA_ERR_ARG;
+  if (o_dtype != MLA_FP32 && o_dtype != dims->dtype) return MLA_ERR_ARG;
+  if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale)) return MLA_ERR_ARG;
+  if (n_tokens == 0) return MLA_OK;
+  if (!counts_ok(dims, n_tokens)) return MLA_ERR_ARG;
+  if (!cu_tokens || !q_cat || !cache_pool || !page_table || !seq_lens || !o_lat)
+    return MLA_ERR_NULL_ARG;
+  if (!aligned(cu_tokens, 4) || !aligned(q_cat, 16) || !aligned(cache_pool, 16) ||
+      !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(o_lat, 16) || !aligned(lse, 4))
+    return MLA_ERR_ALIGN;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MLA_ERR_ALIGN;
+  HostDevice dev;
+  if ((rc = host_device(&dev)) || (rc = set_attributes())) return rc;
+  const ChunkSpace w = chunk_space(dims, n_tokens, num_splits, dev.sms);
+  if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const chunk::Shape shape{n_tokens, dims->batch, dims->n_heads, max_pages,
+                           w.tile_rows, cu_tokens, seq_lens};
+  const chunk::Plan plan{reinterpret_cast<int32_t*>(ws + w.plan), dims->batch, w.max_tiles,
+                         w.parts};
+  float* part_o = reinterpret_cast<float*>(ws + w.part_o);
+  float* part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  host_launch(chunk::plan_kernel, dim3(1), dim3(chunk::kPlanThreads), 0, st, shape, plan, w.parts,
+              dev.status);
+  if ((rc = host_launched())) return rc;
+  if (dims->dtype == MLA_BF16) return MLA_ERR_DIMS;
+  simt::ChunkParams p{shape, plan, num_pages, q_cat, cache_pool, page_table,
+                      resolve_scale(softmax_scale) * kLog2e, o_lat, lse, part_o, part_lse,
+                      dev.status};
+  host_launch(simt::chunk_kernel, dim3(w.parts), dim3(simt::kThreads),
+              simt::Layout<576, 512>::kBytes, st, p);
+  if ((rc = host_launched())) return rc;
+  if (w.parts == 1) return MLA_OK;
+  host_launch(chunk::combine_kernel<float>,
+              dim3(w.parts - 1, w.tile_rows / chunk::kCombineWarps),
+              dim3(32 * chunk::kCombineWarps), 0, st, shape, plan, part_o, part_lse,
+              static_cast<float*>(o_lat), lse);
+  return host_launched();
+}
+
+}  // extern "C"
