@@ -8,6 +8,7 @@
 #include "attn_simt.cuh"
 #include "chunk_plan.cuh"
 #include "host_services.h"
+#include "prompt_sm100.cuh"
 #include "rows.cuh"
 
 namespace mla {
@@ -44,6 +45,9 @@ int set_attributes() {
       (e = cudaFuncSetAttribute(simt::chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(simt::Layout<576, 512>::kBytes))) != cudaSuccess)
     return host_cuda_error(e, "cudaFuncSetAttribute");
+  if ((e = cudaFuncSetAttribute(prompt::prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(prompt::kSmemBytes))) != cudaSuccess)
+    return host_cuda_error(e, "cudaFuncSetAttribute(prompt_kernel)");
   done[dev] = true;
   return MLA_OK;
 }
@@ -174,6 +178,36 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
     return MLA_ERR_ALIGN;
   HostDevice dev;
   if ((rc = host_device(&dev)) || (rc = set_attributes())) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const float scale_log2 = resolve_scale(softmax_scale) * kLog2e;
+  // every sequence has at most one tile that is not full
+  const auto tiles = [&](int rows) {
+    return static_cast<unsigned>(n_tokens / rows + std::min(dims->batch, n_tokens));
+  };
+  if (dims->dtype == MLA_BF16) {
+    // heads x tokens of 64-column boxes of 128 tokens; tokens past n_tokens read as zero
+    const auto map = [&](CUtensorMap* m, const void* base, int width, int heads, int64_t head_stride,
+                         int64_t token_stride) {
+      const uint64_t dim[3] = {static_cast<uint64_t>(width), static_cast<uint64_t>(heads),
+                               static_cast<uint64_t>(n_tokens)};
+      const uint64_t str[2] = {2 * static_cast<uint64_t>(head_stride),
+                               2 * static_cast<uint64_t>(token_stride)};
+      const uint32_t box[3] = {64, 1, prompt::kTile};
+      return host_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dim, str, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    CUtensorMap tq, tk, tkr, tv;
+    if ((rc = map(&tq, q, kDn + kDr, dims->n_heads, q_head_stride, q_token_stride)) ||
+        (rc = map(&tk, k_nope, kDn, n_kv_heads, k_head_stride, k_token_stride)) ||
+        (rc = map(&tkr, k_rope, kDr, 1, k_rope_stride, k_rope_stride)) ||
+        (rc = map(&tv, v, kDv, n_kv_heads, v_head_stride, v_token_stride)))
+      return rc;
+    const prompt::Params p{n_tokens, dims->batch, dims->n_heads, n_kv_heads, cu_tokens, scale_log2,
+                           static_cast<__nv_bfloat16*>(o), lse, dev.status, host_wait_ns()};
+    host_launch(prompt::prompt_kernel, dim3(tiles(prompt::kRows), dims->n_heads),
+                dim3(prompt::kThreads), prompt::kSmemBytes, st, tq, tk, tkr, tv, p);
+    return host_launched();
+  }
   simt::PromptParams p{};
   p.n_tokens = n_tokens;
   p.batch = dims->batch;
@@ -191,16 +225,12 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
   p.kr_tok = k_rope_stride;
   p.v_tok = v_token_stride;
   p.v_head = v_head_stride;
-  p.scale_log2 = resolve_scale(softmax_scale) * kLog2e;
+  p.scale_log2 = scale_log2;
   p.o = o;
   p.lse = lse;
   p.status = dev.status;
-  if (dims->dtype == MLA_BF16) return MLA_ERR_DIMS;
-  // every sequence has at most one tile that is not full
-  const unsigned tiles =
-      static_cast<unsigned>(n_tokens / simt::kRows + std::min(dims->batch, n_tokens));
-  host_launch(simt::prompt_kernel, dim3(tiles, dims->n_heads), dim3(simt::kThreads),
-              simt::Layout<192, 128>::kBytes, reinterpret_cast<cudaStream_t>(stream), p);
+  host_launch(simt::prompt_kernel, dim3(tiles(simt::kRows), dims->n_heads), dim3(simt::kThreads),
+              simt::Layout<192, 128>::kBytes, st, p);
   return host_launched();
 }
 
