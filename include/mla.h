@@ -366,6 +366,7 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
  *   o_lat  [n_tokens, H, d_c] of type o_dtype: dims.dtype, or MLA_FP32 (for mla_out_proj and
  *          mla_merge_partials); on the bf16 path the weights p are rounded to bf16 either way.
  *   lse    [n_tokens, H] fp32, nullable.
+ * What the pool holds behind a sequence's last row has no influence, whatever it is (NaN too).
  * A token that sees no row (n_b > seq_lens[b]) gets o_lat = 0, lse = -inf.  Lengths outside
  * [0, max_pages * page_size] are clamped and raise MLA_STATUS_BAD_LENGTH, page ids out of range
  * read page 0 and raise MLA_STATUS_BAD_PAGE.

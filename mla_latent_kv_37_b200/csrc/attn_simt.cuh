@@ -267,14 +267,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
       const int64_t row = whole ? row0 + r : static_cast<int64_t>(slot) * kRows + r;
       float* dst = (whole ? static_cast<float*>(p.o) : p.part_o) + row * chunk::kDc;
       float* dst_lse = whole ? p.lse : p.part_lse;
-      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // (a NaN stays one)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         chunk::store4(dst + 4 * (lane + 32 * k),
                       make_float4(o[i][4 * k] * inv, o[i][4 * k + 1] * inv,
                                   o[i][4 * k + 2] * inv, o[i][4 * k + 3] * inv));
       if (lane == 0 && dst_lse)
-        dst_lse[row] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -__int_as_float(0x7f800000);
+        dst_lse[row] = l[i] == 0.f ? -__int_as_float(0x7f800000) : (m[i] + log2f(l[i])) * kLn2;
     }
   }
 }

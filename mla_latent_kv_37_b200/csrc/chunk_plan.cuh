@@ -258,13 +258,13 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
       acc[q].w += w * x.w;
     }
   }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;  // (a NaN stays one)
   const int64_t row = static_cast<int64_t>(t.tok0) * s.n_heads + t.row0 + r;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     store4(o + row * kDc + 4 * (lane + 32 * q),
            make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv));
-  if (lane == 0 && lse) lse[row] = tot > 0.f ? m + logf(tot) : NEG_INF;
+  if (lane == 0 && lse) lse[row] = tot == 0.f ? NEG_INF : m + logf(tot);
 }
 
 }  // namespace chunk

@@ -7,6 +7,7 @@
 
 #include "attn_simt.cuh"
 #include "chunk_plan.cuh"
+#include "chunk_sm100.cuh"
 #include "host_services.h"
 #include "prompt_sm100.cuh"
 #include "rows.cuh"
@@ -48,6 +49,9 @@ int set_attributes() {
   if ((e = cudaFuncSetAttribute(prompt::prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(prompt::kSmemBytes))) != cudaSuccess)
     return host_cuda_error(e, "cudaFuncSetAttribute(prompt_kernel)");
+  if ((e = cudaFuncSetAttribute(chunk::pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(chunk::kSmemBytes))) != cudaSuccess)
+    return host_cuda_error(e, "cudaFuncSetAttribute(pair_kernel)");
   done[dev] = true;
   return MLA_OK;
 }
@@ -57,12 +61,11 @@ struct ChunkSpace {
   size_t plan, part_o, part_lse, total;
   int tile_rows, max_tiles, parts;
 };
-int chunk_tile_rows(const mla_dims* d) { return simt::kRows; }
-
 ChunkSpace chunk_space(const mla_dims* d, int n_tokens, int num_splits, int sms) {
   ChunkSpace w{};
-  w.tile_rows = chunk_tile_rows(d);
-  w.parts = num_splits > 0 ? num_splits : sms;
+  const bool bf16 = d->dtype == MLA_BF16;
+  w.tile_rows = bf16 ? chunk::kTileRows : simt::kRows;
+  w.parts = num_splits > 0 ? num_splits : bf16 ? sms / 2 : sms;  // CTA pairs, or CTAs
   const int64_t rows = static_cast<int64_t>(n_tokens) * d->n_heads;
   w.max_tiles = static_cast<int>(rows / w.tile_rows + std::min<int64_t>(d->batch, n_tokens));
   size_t off = 0;
@@ -279,18 +282,40 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
   host_launch(chunk::plan_kernel, dim3(1), dim3(chunk::kPlanThreads), 0, st, shape, plan, w.parts,
               dev.status);
   if ((rc = host_launched())) return rc;
-  if (dims->dtype == MLA_BF16) return MLA_ERR_DIMS;
-  simt::ChunkParams p{shape, plan, num_pages, q_cat, cache_pool, page_table,
-                      resolve_scale(softmax_scale) * kLog2e, o_lat, lse, part_o, part_lse,
-                      dev.status};
-  host_launch(simt::chunk_kernel, dim3(w.parts), dim3(simt::kThreads),
-              simt::Layout<576, 512>::kBytes, st, p);
+  const float scale_log2 = resolve_scale(softmax_scale) * kLog2e;
+  if (dims->dtype == MLA_BF16) {
+    // rows of 576 in boxes of 64 columns x 64 rows: the queries, and the pool's pages
+    const auto map = [&](CUtensorMap* m, const void* base, int64_t rows) {
+      const uint64_t dim[2] = {chunk::kRow, static_cast<uint64_t>(rows)};
+      const uint64_t str[1] = {2 * chunk::kRow};
+      const uint32_t box[2] = {64, 64};
+      return host_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dim, str, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    CUtensorMap tq, tc;
+    if ((rc = map(&tq, q_cat, static_cast<int64_t>(n_tokens) * dims->n_heads)) ||
+        (rc = map(&tc, cache_pool, static_cast<int64_t>(num_pages) * kPageN)))
+      return rc;
+    const chunk::Params p{shape, plan, num_pages, page_table, scale_log2, o_lat,
+                          o_dtype == MLA_FP32, lse, part_o, part_lse, dev.status, host_wait_ns()};
+    host_launch(chunk::pair_kernel, dim3(2 * w.parts), dim3(chunk::kThreads), chunk::kSmemBytes,
+                st, tq, tc, p);
+  } else {
+    const simt::ChunkParams p{shape, plan, num_pages, q_cat, cache_pool, page_table, scale_log2,
+                              o_lat, lse, part_o, part_lse, dev.status};
+    host_launch(simt::chunk_kernel, dim3(w.parts), dim3(simt::kThreads),
+                simt::Layout<576, 512>::kBytes, st, p);
+  }
   if ((rc = host_launched())) return rc;
   if (w.parts == 1) return MLA_OK;
-  host_launch(chunk::combine_kernel<float>,
-              dim3(w.parts - 1, w.tile_rows / chunk::kCombineWarps),
-              dim3(32 * chunk::kCombineWarps), 0, st, shape, plan, part_o, part_lse,
-              static_cast<float*>(o_lat), lse);
+  const dim3 grid(w.parts - 1, w.tile_rows / chunk::kCombineWarps);
+  const dim3 block(32 * chunk::kCombineWarps);
+  if (o_dtype == MLA_FP32)
+    host_launch(chunk::combine_kernel<float>, grid, block, 0, st, shape, plan, part_o, part_lse,
+                static_cast<float*>(o_lat), lse);
+  else
+    host_launch(chunk::combine_kernel<__nv_bfloat16>, grid, block, 0, st, shape, plan, part_o,
+                part_lse, static_cast<__nv_bfloat16*>(o_lat), lse);
   return host_launched();
 }
 
