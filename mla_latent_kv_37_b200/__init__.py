@@ -168,19 +168,6 @@ def _need(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _need_table(t, d: mla_dims):
-    _need(t, "page_table", torch.int32)
-    if t.dim() != 2 or t.shape[0] != d.batch:
-        raise ValueError(f"page_table must have shape ({d.batch}, max_pages), got {tuple(t.shape)}")
-
-
-def _need_pool(t, d: mla_dims):
-    _need(t, "cache_pool", _elem(d))
-    if t.dim() != 3 or t.shape[1:] != (d.page_size, d.d_c + d.d_rope):
-        raise ValueError(f"cache_pool must have shape (num_pages, {d.page_size}, "
-                         f"{d.d_c + d.d_rope}), got {tuple(t.shape)}")
-
-
 def _elem(d: mla_dims):
     return torch.bfloat16 if d.dtype == MLA_BF16 else torch.float32
 
@@ -314,35 +301,71 @@ def mla_out_proj(d: mla_dims, o_lat, w_uv, ws, w_o=None, o_heads=None, out=None,
 # ---------------------------------------------------------------------------------------------
 # several new tokens per sequence
 # ---------------------------------------------------------------------------------------------
-def _need_view(t, name, dtype, shape):
-    """A CUDA tensor of this type and shape whose last dimension is contiguous; the strides of the
-    others are the library's to check."""
+# These calls are also the smallest ones (a few tokens, a few microseconds on the GPU), so a tensor's
+# checks are one expression, and what is wrong is worked out only where something is.
+def _refuse(t, name, dtype, shape, dev):
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
                          f"{tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.numel() and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if t.get_device() != dev:
+        raise ValueError(f"tensors must be on one device, got cuda:{dev} and {t.device} ({name})")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _strides(t):
-    """Strides of the leading dimensions.  Where a dimension has one element, torch's stride says
-    nothing: the distance that a contiguous tensor would have stands in."""
-    out, least = [], t.shape[-1]
-    for i in range(t.dim() - 2, -1, -1):
-        s = t.stride(i) if t.shape[i] > 1 else least
-        out.append(s)
-        least = max(least, s * t.shape[i])
-    return out[::-1]
+def _at(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _one_device(*tensors):
-    """All tensors on the current device, which is where the library launches."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+def _rows_at(t, name, dtype, shape, dev):
+    """Address and row stride of [T, width], whose rows are contiguous; the stride is the library's
+    to check.  Where a dimension has one element, torch's stride says nothing: the distance that a
+    contiguous tensor would have stands in."""
+    s0, s1 = t.stride() if t.dim() == 2 else (0, 0)
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
+            (s1 == 1 or not t.numel())):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+
+
+def _heads_at(t, name, dtype, shape, dev):
+    """The same of [T, heads, width]: address, token stride, head stride."""
+    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
+            (s2 == 1 or not t.numel())):
+        _refuse(t, name, dtype, shape, dev)
+    n, h, w = shape
+    if h == 1:
+        s1 = w
+    return t.data_ptr(), s0 if n > 1 else max(w, h * s1), s1
+
+
+def _pool_at(t, dtype, dev):
+    shape = t.shape
+    if t.dim() != 3:
+        raise ValueError(f"cache_pool must have shape (num_pages, 64, 576), got {tuple(shape)}")
+    return _at(t, "cache_pool", dtype, (shape[0], 64, 576), dev), shape[0]
+
+
+def _table_at(t, batch, dev):
+    shape = t.shape
+    if t.dim() != 2:
+        raise ValueError(f"page_table must have shape ({batch}, max_pages), got {tuple(shape)}")
+    return _at(t, "page_table", torch.int32, (batch, shape[1]), dev), shape[1]
+
+
+def _stream_on(dev, stream):
+    """The stream's handle; the library launches on the current device, so the tensors' has to be it."""
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current device cuda:{torch.cuda.current_device()}, "
+                         f"got cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def mla_append_rows(d: mla_dims, c_kv, k_r, cu_tokens, seq_lens, page_table, cache_pool, k_rope=None,
@@ -352,27 +375,24 @@ def mla_append_rows(d: mla_dims, c_kv, k_r, cu_tokens, seq_lens, page_table, cac
     c_kv [T, 512] and k_r [T, 64] of the packed tokens, cu_tokens [batch + 1], seq_lens [batch]
     (rows with the new tokens).  k_rope [T, 64] also receives the rotated keys; q_rope [T, H, 64]
     (a view of the queries) is rotated into q_rope_out (itself, or a view of q_cat)."""
-    e, T = _elem(d), c_kv.shape[0]
-    _need_view(c_kv, "c_kv", e, (T, d.d_c))
-    _need_view(k_r, "k_r", e, (T, d.d_rope))
-    _need(cu_tokens, "cu_tokens", torch.int32, (d.batch + 1,))
-    _need(seq_lens, "seq_lens", torch.int32, (d.batch,))
-    _need_table(page_table, d)
-    _need_pool(cache_pool, d)
-    _need(k_rope, "k_rope", e, (T, d.d_rope))
+    e, T, B = _elem(d), c_kv.shape[0], d.batch
+    dev = c_kv.get_device()
+    c, cs = _rows_at(c_kv, "c_kv", e, (T, 512), dev)
+    k, ks = _rows_at(k_r, "k_r", e, (T, 64), dev)
+    cu = _at(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
+    lens = _at(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    table, max_pages = _table_at(page_table, B, dev)
+    pool, num_pages = _pool_at(cache_pool, e, dev)
+    kr = None if k_rope is None else _at(k_rope, "k_rope", e, (T, 64), dev)
     if (q_rope is None) != (q_rope_out is None):
         raise ValueError("q_rope and q_rope_out go together")
-    qs = qo = (0, 0)
+    q = qo = (None, 0, 0)
     if q_rope is not None:
-        _need_view(q_rope, "q_rope", e, (T, d.n_heads, d.d_rope))
-        _need_view(q_rope_out, "q_rope_out", e, (T, d.n_heads, d.d_rope))
-        qs, qo = _strides(q_rope), _strides(q_rope_out)
-    _one_device(c_kv, k_r, cu_tokens, seq_lens, page_table, cache_pool, k_rope, q_rope, q_rope_out)
-    rc = lib().mla_append_rows(
-        ctypes.byref(d), T, _ptr(cu_tokens), _ptr(seq_lens), _ptr(c_kv), _strides(c_kv)[0],
-        _ptr(k_r), _strides(k_r)[0], _ptr(page_table), page_table.shape[1], _ptr(cache_pool),
-        cache_pool.shape[0], _ptr(k_rope), _ptr(q_rope), qs[0], qs[1], _ptr(q_rope_out), qo[0],
-        qo[1], _stream(stream))
+        shape = (T, d.n_heads, 64)
+        q = _heads_at(q_rope, "q_rope", e, shape, dev)
+        qo = _heads_at(q_rope_out, "q_rope_out", e, shape, dev)
+    rc = lib().mla_append_rows(ctypes.byref(d), T, cu, lens, c, cs, k, ks, table, max_pages, pool,
+                               num_pages, kr, *q, *qo, _stream_on(dev, stream))
     _check(rc, "mla_append_rows")
 
 
@@ -383,19 +403,16 @@ def mla_prompt_attn(d: mla_dims, q, k_nope, k_rope, v, cu_tokens, o, lse=None,
     lse [T, H].  q, k_nope, k_rope and v may be views with strides of 16-byte multiples."""
     e, T, H = _elem(d), q.shape[0], d.n_heads
     Hk = k_nope.shape[1] if k_nope.dim() == 3 else 0
-    _need_view(q, "q", e, (T, H, d.d_nope + d.d_rope))
-    _need_view(k_nope, "k_nope", e, (T, Hk, d.d_nope))
-    _need_view(k_rope, "k_rope", e, (T, d.d_rope))
-    _need_view(v, "v", e, (T, Hk, d.d_v))
-    _need(cu_tokens, "cu_tokens", torch.int32, (d.batch + 1,))
-    _need(o, "o", e, (T, H, d.d_v))
-    _need(lse, "lse", torch.float32, (T, H))
-    _one_device(q, k_nope, k_rope, v, cu_tokens, o, lse)
-    qs, ks, vs = _strides(q), _strides(k_nope), _strides(v)
-    rc = lib().mla_prompt_attn(
-        ctypes.byref(d), T, Hk, _ptr(cu_tokens), _ptr(q), qs[0], qs[1], _ptr(k_nope), ks[0], ks[1],
-        _ptr(k_rope), _strides(k_rope)[0], _ptr(v), vs[0], vs[1], float(softmax_scale), _ptr(o),
-        _ptr(lse), _stream(stream))
+    dev = q.get_device()
+    q = _heads_at(q, "q", e, (T, H, 192), dev)
+    k = _heads_at(k_nope, "k_nope", e, (T, Hk, 128), dev)
+    kr = _rows_at(k_rope, "k_rope", e, (T, 64), dev)
+    v = _heads_at(v, "v", e, (T, Hk, 128), dev)
+    cu = _at(cu_tokens, "cu_tokens", torch.int32, (d.batch + 1,), dev)
+    o = _at(o, "o", e, (T, H, 128), dev)
+    l = None if lse is None else _at(lse, "lse", torch.float32, (T, H), dev)
+    rc = lib().mla_prompt_attn(ctypes.byref(d), T, Hk, cu, *q, *k, *kr, *v, softmax_scale, o, l,
+                               _stream_on(dev, stream))
     _check(rc, "mla_prompt_attn")
 
 
@@ -415,21 +432,22 @@ def mla_chunk_attn(d: mla_dims, q_cat, cache_pool, page_table, cu_tokens, seq_le
     """Attention of several new tokens per sequence over the paged latent cache, which holds their
     own rows already: q_cat [T, H, 576] -> o_lat [T, H, 512] (the cache's type, or fp32 for
     mla_out_proj), lse [T, H].  `ws` from chunk_workspace(d, T, num_splits)."""
-    e, T, H = _elem(d), q_cat.shape[0], d.n_heads
-    _need(q_cat, "q_cat", e, (T, H, d.d_c + d.d_rope))
-    _need_pool(cache_pool, d)
-    _need_table(page_table, d)
-    _need(cu_tokens, "cu_tokens", torch.int32, (d.batch + 1,))
-    _need(seq_lens, "seq_lens", torch.int32, (d.batch,))
-    _need(o_lat, "o_lat", None if o_lat.dtype == e else torch.float32, (T, H, d.d_c))
-    _need(lse, "lse", torch.float32, (T, H))
-    _need(ws, "workspace", torch.uint8)
-    _one_device(q_cat, cache_pool, page_table, cu_tokens, seq_lens, o_lat, lse, ws)
-    rc = lib().mla_chunk_attn(
-        ctypes.byref(d), T, _ptr(cu_tokens), _ptr(q_cat), _ptr(cache_pool), cache_pool.shape[0],
-        _ptr(page_table), page_table.shape[1], _ptr(seq_lens), float(softmax_scale),
-        int(num_splits), _ptr(ws), ws.numel(), _ptr(o_lat),
-        MLA_FP32 if o_lat.dtype == torch.float32 else MLA_BF16, _ptr(lse), _stream(stream))
+    e, T, H, B = _elem(d), q_cat.shape[0], d.n_heads, d.batch
+    dev = q_cat.get_device()
+    q = _at(q_cat, "q_cat", e, (T, H, 576), dev)
+    pool, num_pages = _pool_at(cache_pool, e, dev)
+    table, max_pages = _table_at(page_table, B, dev)
+    cu = _at(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
+    lens = _at(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    o_type = o_lat.dtype
+    o = _at(o_lat, "o_lat", e if o_type is e else torch.float32, (T, H, 512), dev)
+    l = None if lse is None else _at(lse, "lse", torch.float32, (T, H), dev)
+    n_ws = ws.numel()
+    w = _at(ws, "workspace", torch.uint8, (n_ws,), dev)
+    rc = lib().mla_chunk_attn(ctypes.byref(d), T, cu, q, pool, num_pages, table, max_pages, lens,
+                              softmax_scale, num_splits, w, n_ws, o,
+                              MLA_FP32 if o_type is torch.float32 else MLA_BF16, l,
+                              _stream_on(dev, stream))
     _check(rc, "mla_chunk_attn")
 
 
