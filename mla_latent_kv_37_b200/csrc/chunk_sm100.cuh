@@ -190,9 +190,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (b0 == b1) continue;
       const int32_t* table = p.page_table + static_cast<int64_t>(t.seq) * p.shape.max_pages;
       const int pages = (t.visible(t.rows - 1, H) + kPage - 1) / kPage;
-      if (keys && lane == 0) {
-        if (sg > 0) ok = mbar_wait(&bars->q_empty, (sg - 1) & 1, wc);
-        if (ok) {
+      if (keys) {
+        if (sg > 0) ok = warp_wait(&bars->q_empty, (sg - 1) & 1, wc);
+        if (ok && elect_one()) {
           const uint32_t bar = mapa_shared(smem_u32(&bars->q_full), 0);
           if (rank == 0) mbar_arrive_expect_tx(&bars->q_full, 2 * 9 * kBoxBytes);
           const int y = t.tok0 * H + t.row0 + static_cast<int>(rank) * kCtaRows;
@@ -200,7 +200,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             pair_load_2d(smem + kOffQ + c * kBoxBytes, &tm_q, bar, 64 * c, y);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int b = b0; ok && b < b1; b += 16) {
         // the next 32 page ids; a block's second page may lie past the last one and then is the
         // first again (its keys are masked, and its values cleared like those past the end)
@@ -216,36 +215,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // keys of this block that the sequence holds
           const int held = t.len - (b + k) * kBlock;
           const bool ragged = held < kBlock;
-          if (lane == 0) {
-            if (keys) {
-              for (int u = 0; ok && u < kKUnits; ++u) {
-                if (n > 0) ok = mbar_wait(&bars->k_empty[u], (n - 1) & 1, wc);
-                if (!ok) break;
+          if (keys) {
+            const int y = rank ? y1 : y0;
+#pragma unroll
+            for (int u = 0; u < kKUnits; ++u) {
+              if (ok && n > 0) ok = warp_wait(&bars->k_empty[u], (n - 1) & 1, wc);
+              if (ok && elect_one()) {
                 if (rank == 0) mbar_arrive_expect_tx(&bars->k_full[u], 2 * kKUnit);
                 const uint32_t bar = mapa_shared(smem_u32(&bars->k_full[u]), 0);
+#pragma unroll
                 for (int c = 0; c < 3; ++c)
                   pair_load_2d(smem + kOffK + u * kKUnit + c * kBoxBytes, &tm_c, bar,
-                               64 * (3 * u + c), rank ? y1 : y0);
-              }
-            } else {
-              for (int u = 0; ok && u < kVUnits; ++u) {
-                if (n > 0) ok = mbar_wait(&bars->v_empty[u], (n - 1) & 1, wc);
-                if (!ok) break;
-                const uint32_t bar = ragged ? smem_u32(&bars->v_tail[u])
-                                            : mapa_shared(smem_u32(&bars->v_full[u]), 0);
-                if (ragged)
-                  mbar_arrive_expect_tx(&bars->v_tail[u], kVUnit);
-                else
-                  arrive_expect_tx_cluster(bar, kVUnit);
-                for (int c = 0; c < 2; ++c)
-                  pair_load_2d(smem + kOffV + u * kVUnit + c * kBoxBytes, &tm_c, bar,
-                               256 * (u & 1) + 128 * static_cast<int>(rank) + 64 * c,
-                               u >> 1 ? y1 : y0);
+                               64 * (3 * u + c), y);
               }
             }
+            continue;
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (keys || !ragged) continue;
+#pragma unroll
+          for (int u = 0; u < kVUnits; ++u) {
+            if (ok && n > 0) ok = warp_wait(&bars->v_empty[u], (n - 1) & 1, wc);
+            if (ok && elect_one()) {
+              const uint32_t bar = ragged ? smem_u32(&bars->v_tail[u])
+                                          : mapa_shared(smem_u32(&bars->v_full[u]), 0);
+              arrive_expect_tx_cluster(bar, kVUnit);
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                pair_load_2d(smem + kOffV + u * kVUnit + c * kBoxBytes, &tm_c, bar,
+                             256 * (u & 1) + 128 * static_cast<int>(rank) + 64 * c,
+                             u >> 1 ? y1 : y0);
+            }
+          }
+          if (!ragged) continue;
           // what the pool holds past the sequence's end must not reach the product: a weight of
           // zero does not silence a NaN
           for (int u = 0; ok && u < kVUnits; ++u) {
@@ -276,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 5) {
     // =================== MMA issuer (the leader's) ===================
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       const uint32_t id_s = idesc_bf16(kTileRows, kBlock, 0, 0);
       const uint32_t id_o = idesc_bf16(kTileRows, 256, 0, 1);
       const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
@@ -285,51 +285,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t d_v = smem_desc(smem_u32(smem + kOffV), kBoxBytes, 1024, kSwizzle128B);
       const auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
       bool ok = true;
-      const auto issue_s = [&](int n) {
-        if (n >= 2) ok = mbar_wait<true>(&bars->s_free[n & 1], ((n >> 1) - 1) & 1, wc);
-        for (int u = 0; ok && u < kKUnits; ++u) {
-          if (!(ok = mbar_wait(&bars->k_full[u], n & 1, wc))) break;
+      const auto issue_s = [&](int n, bool last) {
+        if (n >= 2) ok = warp_wait<true>(&bars->s_free[n & 1], ((n >> 1) - 1) & 1, wc);
+#pragma unroll
+        for (int u = 0; u < kKUnits; ++u) {
+          ok = ok && warp_wait(&bars->k_full[u], n & 1, wc);
+          if (!ok) return;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int c = 0; c < 3; ++c)
+            for (int c = 0; c < 3; ++c)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pair_mma_ss(tmem + kTmemS + 64 * (n & 1), at(d_q, (3 * u + c) * kBoxBytes + 32 * k),
-                          at(d_k, u * kKUnit + c * kBoxBytes + 32 * k), id_s,
-                          u > 0 || c > 0 || k > 0);
-          pair_commit(&bars->k_empty[u]);
+              for (int k = 0; k < 4; ++k)
+                pair_mma_ss(tmem + kTmemS + 64 * (n & 1),
+                            at(d_q, (3 * u + c) * kBoxBytes + 32 * k),
+                            at(d_k, u * kKUnit + c * kBoxBytes + 32 * k), id_s,
+                            u > 0 || c > 0 || k > 0);
+            pair_commit(&bars->k_empty[u]);
+            if (u == kKUnits - 1) {
+              pair_commit(&bars->s_full[n & 1]);
+              if (last) pair_commit(&bars->q_empty);
+            }
+          }
         }
-        if (ok) pair_commit(&bars->s_full[n & 1]);
       };
       const auto issue_o = [&](int n, bool first) {
-        ok = mbar_wait<true>(&bars->p_full, n & 1, wc);
-        for (int u = 0; ok && u < kVUnits; ++u) {
-          if (!(ok = mbar_wait<true>(&bars->v_full[u], n & 1, wc))) break;
-          tc_fence_after();
+        ok = ok && warp_wait<true>(&bars->p_full, n & 1, wc);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            pair_mma_ss(tmem + kTmemO + 128 * (u & 1), at(d_p, (u >> 1) * kBoxBytes + 32 * k),
-                        at(d_v, u * kVUnit + 2048 * k), id_o, !first || u > 1 || k > 0);
-          pair_commit(&bars->v_empty[u]);
+        for (int u = 0; u < kVUnits; ++u) {
+          ok = ok && warp_wait<true>(&bars->v_full[u], n & 1, wc);
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pair_mma_ss(tmem + kTmemO + 128 * (u & 1), at(d_p, (u >> 1) * kBoxBytes + 32 * k),
+                          at(d_v, u * kVUnit + 2048 * k), id_o, u > 1 || k > 0 || !first);
+            pair_commit(&bars->v_empty[u]);
+            if (u == kVUnits - 1) pair_commit(&bars->pv_done);
+          }
         }
-        if (ok) pair_commit(&bars->pv_done);
       };
       int n = 0, sg = 0;  // S issued, non-empty segments begun
       while (ok && it.next(t, tile, b0, b1, blocks)) {
         if (b0 == b1) continue;
-        ok = mbar_wait(&bars->q_full, sg & 1, wc);
-        if (ok) issue_s(n);
+        ok = warp_wait(&bars->q_full, sg & 1, wc);
+        if (ok) issue_s(n, b0 + 1 == b1);
         for (int b = b0; ok && b < b1; ++b, ++n) {
-          if (b + 1 < b1)
-            issue_s(n + 1);
-          else
-            pair_commit(&bars->q_empty);
-          if (ok && b == b0 && sg > 0) ok = mbar_wait<true>(&bars->o_free, (sg - 1) & 1, wc);
+          if (b + 1 < b1) issue_s(n + 1, b + 2 == b1);
+          if (ok && b == b0 && sg > 0) ok = warp_wait<true>(&bars->o_free, (sg - 1) & 1, wc);
           if (ok) issue_o(n, b == b0);
         }
         ++sg;
       }
-      pair_commit(&bars->drain);
+      if (elect_one()) pair_commit(&bars->drain);
       mbar_wait(&bars->drain, 0, drain_ctx);
     }
   } else {

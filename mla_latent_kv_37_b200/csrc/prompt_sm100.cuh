@@ -128,106 +128,121 @@ __global__ void __maxnreg__(168)
 
   if (warp == 8) {
     // =================== TMA producer ===================
-    if (lane == 0) {
-      bool ok = true;
-      int kb = 0, vb = 0;
-      const auto load_q = [&](int t) {
+    bool ok = true;
+    int kb = 0, vb = 0;
+    const auto load_q = [&](int t) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(&bars->q_full[t], 3 * kBox);
+#pragma unroll
         for (int c = 0; c < 3; ++c)
           tma_load_3d(smem + kOffQ + (3 * t + c) * kBox, &tm_q, &bars->q_full[t], 64 * c, h,
                       sp.begin + q0 + t * kTile);
-      };
-      load_q(0);
-      for (int j = 0; ok && j < n_max; ++j) {
-        const int y = sp.begin + j * kTile;
-        for (int c = 0; ok && c < 3; ++c, ++kb) {
-          const int s = kb % kKSlots;
-          if (kb >= kKSlots) ok = mbar_wait(&bars->k_empty[s], (kb / kKSlots - 1) & 1, wc);
-          if (!ok) break;
+      }
+    };
+    load_q(0);
+    for (int j = 0; ok && j < n_max; ++j) {
+      const int y = sp.begin + j * kTile;
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const int s = kb % kKSlots;
+        if (kb >= kKSlots) ok = ok && warp_wait(&bars->k_empty[s], (kb / kKSlots - 1) & 1, wc);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&bars->k_full[s], kBox);
           if (c < 2)
             tma_load_3d(smem + kOffK + s * kBox, &tm_k, &bars->k_full[s], 64 * c, hk, y);
           else
             tma_load_3d(smem + kOffK + s * kBox, &tm_kr, &bars->k_full[s], 0, 0, y);
         }
-        if (j == 0 && n1 > 0) load_q(1);
-        if (ok) {
-          const int s = vb % kVSlots;
-          if (vb >= kVSlots) ok = mbar_wait(&bars->v_empty[s], (vb / kVSlots - 1) & 1, wc);
-          if (!ok) break;
+        ++kb;
+      }
+      if (j == 0 && n1 > 0) load_q(1);
+      if (ok) {
+        const int s = vb % kVSlots;
+        if (vb >= kVSlots) ok = warp_wait(&bars->v_empty[s], (vb / kVSlots - 1) & 1, wc);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&bars->v_full[s], 2 * kBox);
+#pragma unroll
           for (int c = 0; c < 2; ++c)
             tma_load_3d(smem + kOffV + (2 * s + c) * kBox, &tm_v, &bars->v_full[s], 64 * c, hk, y);
-          ++vb;
         }
+        ++vb;
       }
-      // no copy may still be landing when the CTA exits (after an abort some may be in flight)
-      mbar_wait(&bars->q_full[0], 0, drain_ctx);
-      if (n1 > 0 && kb > 0) mbar_wait(&bars->q_full[1], 0, drain_ctx);
-      for (int i = max(0, kb - kKSlots); i < kb; ++i)
-        mbar_wait(&bars->k_full[i % kKSlots], (i / kKSlots) & 1, drain_ctx);
-      for (int i = max(0, vb - kVSlots); i < vb; ++i)
-        mbar_wait(&bars->v_full[i % kVSlots], (i / kVSlots) & 1, drain_ctx);
     }
+    // no copy may still be landing when the CTA exits (after an abort some may be in flight)
+    mbar_wait(&bars->q_full[0], 0, drain_ctx);
+    if (n1 > 0 && kb > 0) mbar_wait(&bars->q_full[1], 0, drain_ctx);
+    for (int i = max(0, kb - kKSlots); i < kb; ++i)
+      mbar_wait(&bars->k_full[i % kKSlots], (i / kKSlots) & 1, drain_ctx);
+    for (int i = max(0, vb - kVSlots); i < vb; ++i)
+      mbar_wait(&bars->v_full[i % kVSlots], (i / kVSlots) & 1, drain_ctx);
   } else if (warp == 9) {
     // =================== MMA issuer ===================
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16(kTile, kTile, 0, 0), id_o = idesc_bf16(kTile, 128, 0, 1);
-      const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
-      const uint64_t d_k = smem_desc(smem_u32(smem + kOffK), 16, 1024, kSwizzle128B);
-      const uint64_t d_v = smem_desc(smem_u32(smem + kOffV), kBox, 1024, kSwizzle128B);
-      const auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
-      bool ok = true;
-      // S_t(j); the first tile to use a key box waits for it, the last one releases it
-      const auto issue_s = [&](int t, int j) {
-        const bool first = t == 0 || j >= n0, last = t == 1 || j >= n1;
-        if (j == 0) ok = ok && mbar_wait(&bars->q_full[t], 0, wc);
-        for (int c = 0; ok && c < 3; ++c) {
-          const int kb = 3 * j + c, s = kb % kKSlots;
-          if (first) {
-            ok = mbar_wait(&bars->k_full[s], (kb / kKSlots) & 1, wc);
-            tc_fence_after();
-            if (!ok) break;
-          }
+    const uint32_t id_s = idesc_bf16(kTile, kTile, 0, 0), id_o = idesc_bf16(kTile, 128, 0, 1);
+    const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
+    const uint64_t d_k = smem_desc(smem_u32(smem + kOffK), 16, 1024, kSwizzle128B);
+    const uint64_t d_v = smem_desc(smem_u32(smem + kOffV), kBox, 1024, kSwizzle128B);
+    const auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
+    bool ok = true;
+    // S_t(j); the first tile to use a key box waits for it, the last one releases it
+    const auto issue_s = [&](int t, int j) {
+      const bool first = t == 0 || j >= n0, last = t == 1 || j >= n1;
+      if (j == 0) ok = ok && warp_wait(&bars->q_full[t], 0, wc);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const int kb = 3 * j + c, s = kb % kKSlots;
+        if (first) ok = ok && warp_wait(&bars->k_full[s], (kb / kKSlots) & 1, wc);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
           const uint64_t a = at(d_q, (3 * t + c) * kBox), b = at(d_k, s * kBox);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ss(tmem + kTmemS + kTile * t, at(a, 32 * k), at(b, 32 * k), id_s, c > 0 || k > 0);
           if (last) mma_commit(&bars->k_empty[s]);
-        }
-        if (ok) mma_commit(&bars->s_full[t]);
-      };
-      const auto issue_pv = [&](int t, int j) {
-        const bool first = t == 0 || j >= n0, last = t == 1 || j >= n1;
-        const int s = j % kVSlots;
-        if (first) ok = ok && mbar_wait(&bars->v_full[s], (j / kVSlots) & 1, wc);
-        ok = ok && mbar_wait(&bars->p_full[t], j & 1, wc);
-        if (!ok) return;
-        tc_fence_after();
-        const int steps = (min(kTile, len - j * kTile) + 15) / 16;
-        const uint64_t b = at(d_v, 2 * s * kBox);
-        for (int k = 0; k < steps; ++k)
-          mma_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + kTile * t + 8 * k, at(b, 2048 * k), id_o,
-                 j > 0 || k > 0);
-        if (last) mma_commit(&bars->v_empty[s]);
-        if (j == (t ? n1 : n0) - 1) mma_commit(&bars->o_full[t]);
-      };
-      issue_s(0, 0);
-      if (n1 > 0) issue_s(1, 0);
-      for (int j = 0; ok && j < n_max; ++j) {
-        if (j < n0) {
-          issue_pv(0, j);
-          if (j + 1 < n0) issue_s(0, j + 1);
-        }
-        if (j < n1) {
-          issue_pv(1, j);
-          if (j + 1 < n1) issue_s(1, j + 1);
+          if (c == 2) mma_commit(&bars->s_full[t]);
         }
       }
-      // no MMA may be in flight when TMEM is released
-      mma_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0, drain_ctx);
+    };
+    const auto issue_pv = [&](int t, int j) {
+      const bool first = t == 0 || j >= n0, last = t == 1 || j >= n1;
+      const int s = j % kVSlots;
+      if (first) ok = ok && warp_wait(&bars->v_full[s], (j / kVSlots) & 1, wc);
+      ok = ok && warp_wait(&bars->p_full[t], j & 1, wc);
+      if (!ok) return;
+      tc_fence_after();
+      const int steps = (min(kTile, len - j * kTile) + 15) / 16;
+      if (elect_one()) {
+        const uint64_t b = at(d_v, 2 * s * kBox);
+        const uint32_t o = tmem + kTmemO + 128 * t, a = tmem + kTmemS + kTile * t;
+        if (steps == kTile / 16) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, j > 0 || k > 0);
+        } else {
+          for (int k = 0; k < steps; ++k)
+            mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, j > 0 || k > 0);
+        }
+        if (last) mma_commit(&bars->v_empty[s]);
+        if (j == (t ? n1 : n0) - 1) mma_commit(&bars->o_full[t]);
+      }
+    };
+    issue_s(0, 0);
+    if (n1 > 0) issue_s(1, 0);
+    for (int j = 0; ok && j < n_max; ++j) {
+      if (j < n0) {
+        issue_pv(0, j);
+        if (ok && j + 1 < n0) issue_s(0, j + 1);
+      }
+      if (ok && j < n1) {
+        issue_pv(1, j);
+        if (ok && j + 1 < n1) issue_s(1, j + 1);
+      }
     }
+    // no MMA may be in flight when TMEM is released
+    if (elect_one()) mma_commit(&bars->drain);
+    mbar_wait(&bars->drain, 0, drain_ctx);
   } else {
     // =================== softmax: warps 4t ... 4t + 3 own tile t, a thread one row ==========
     const int t = warp >> 2, n = t ? n1 : n0;

@@ -283,6 +283,20 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
+// True in one lane of a converged warp, the same one each time.  A warp that issues MMAs or copies
+// stays converged and lets one lane issue under this predicate: the compiler then keeps
+// descriptors and coordinates in uniform registers.  Under `if (lane == 0)` it cannot, and every
+// tcgen05.mma takes about 77 clocks to issue (64 is what a 128 x 128 x 16 product takes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Arrive on a local mbarrier once every tcgen05 operation issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
