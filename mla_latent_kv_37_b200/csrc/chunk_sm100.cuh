@@ -111,13 +111,17 @@ __device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* m, ui
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(leader_bar)
       : "memory");
 }
-// Arrive at a barrier of either CTA, ordering this thread's writes before it for the cluster.
+// Arrive at a barrier of either CTA.  What the arrival announces (P, cleared values) is written and
+// read in the arriving CTA's own shared memory, by its own tensor core, and fenced for it before;
+// so the order within the CTA is enough.  (A release for the cluster waits until all earlier
+// operations of the thread, copies too, are visible there: about 1200 clocks in the value
+// producer, 5.8 ms against 4.3 ms for 1024 tokens over 16384.)
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// Announces bytes to come; says nothing of what was done before.
 __device__ __forceinline__ void arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
                    cluster_addr),
                "r"(bytes)
                : "memory");
