@@ -2,13 +2,14 @@
 //
 // The query rows of a sequence, (token, head) pairs with the head running fastest, are cut into
 // tiles of `tile_rows` rows; a tile attends to the keys its last row sees.  The list of all
-// tiles' key blocks (kBlock keys each) is cut into `parts` ranges of equal cost, one for each
+// tiles' key blocks (block_keys keys each) is cut into `parts` ranges of equal cost, one for each
 // resident CTA (pair): few rows over long caches spread over the machine (split-KV), many rows
 // stay whole.  A range may end inside a tile; the parts of such a tile write normalised partial
 // results with their log-sum-exp, which combine_kernel merges in the order of the parts, so the
 // result does not depend on timing.
 //
-// Cost: a tile's start-up (query load, drained pipeline, write-back) counts as kSegBlocks blocks.
+// Cost of a tile, in units of the kernel's choice: its start-up (query load, drained pipeline,
+// write-back) and its key blocks.
 #pragma once
 #include "packed.cuh"
 #include "ptx_sm100.cuh"
@@ -17,8 +18,6 @@ namespace mla {
 namespace chunk {
 
 constexpr int kPage = 64, kRow = 576, kDc = 512;
-constexpr int kBlock = 128;    // keys per block: two pages
-constexpr int kSegBlocks = 2;  // a tile's start-up in blocks
 constexpr int kPlanThreads = 1024;
 
 // Plan in the workspace, written by plan_kernel.
@@ -40,6 +39,7 @@ struct Plan {
 // What a plan is made for.
 struct Shape {
   int n_tokens, batch, n_heads, max_pages, tile_rows;
+  int block_keys, block_cost, seg_cost;
   const int32_t* cu;
   const int32_t* seq_lens;
 };
@@ -56,8 +56,8 @@ struct Tile {
   __device__ int visible(int r, int n_heads) const {
     return min(max(first + (row0 + r) / n_heads + 1, 0), len);
   }
-  __device__ int blocks(int n_heads) const {
-    return (visible(rows - 1, n_heads) + kBlock - 1) / kBlock;
+  __device__ int blocks(const Shape& s) const {
+    return (visible(rows - 1, s.n_heads) + s.block_keys - 1) / s.block_keys;
   }
 };
 __device__ __forceinline__ Tile tile_at(const Shape& s, const Plan& plan, int i) {
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   griddep_launch_dependents();
   griddep_wait();
   const int T = kPlanThreads, tid = threadIdx.x;
-  const int64_t max_tiles = plan.max_tiles, least = kSegBlocks + 1;
+  const int64_t max_tiles = plan.max_tiles, least = s.seg_cost + s.block_cost;
   int64_t total;
   int n_tiles = 0;
   bool bad = false;
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         if (plan.seq_tile()[mid] <= i) lo = mid; else hi = mid;
       }
       plan.tile_seq()[i] = lo;
-      cost = kSegBlocks + tile_at(s, plan, i).blocks(s.n_heads);
+      cost = s.seg_cost + static_cast<int64_t>(s.block_cost) * tile_at(s, plan, i).blocks(s);
     }
     const int64_t at = block_scan(cost, warp_sums, &total) + v;
     if (i < n_tiles) plan.vstart()[i] = at;
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   if (tid == 0) plan.vstart()[n_tiles] = v;
   __syncthreads();
-  // part c begins at virtual place floor(c V / C).  No part is worth less than a start-up.
+  // part c begins at virtual place floor(c V / C).  No part is worth less than a start-up and a
+  // block, so no two of them begin at the same block.
   const int64_t V = v;
   const int64_t most = V / least;
   const int C = most < 1 ? 1 : most < parts_req ? static_cast<int>(most) : parts_req;
@@ -159,7 +160,8 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (u >= v1) break;
       if (u < v0) continue;
       plan.part_tile()[c] = i;
-      plan.part_block()[c] = u - v0 > kSegBlocks ? static_cast<int>(u - v0 - kSegBlocks) : 0;
+      plan.part_block()[c] =
+          u - v0 > s.seg_cost ? static_cast<int>((u - v0 - s.seg_cost) / s.block_cost) : 0;
     }
   }
   for (int c = tid; c <= plan.max_parts; c += T)
@@ -190,7 +192,7 @@ struct SegIter {
     if (i > i_end || (i == i_end && b >= b_end)) return false;
     tile = i;
     t = tile_at(*s, plan, i);
-    blocks = t.blocks(s->n_heads);
+    blocks = t.blocks(*s);
     b0 = b;
     b1 = i < i_end ? blocks : b_end;
     ++i;

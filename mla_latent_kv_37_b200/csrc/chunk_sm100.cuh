@@ -32,6 +32,8 @@ namespace mla {
 namespace chunk {
 
 constexpr int kTileRows = 128, kCtaRows = 64;
+constexpr int kBlock = 128;  // keys per block: two pages
+constexpr int kBlockCost = 1, kSegCost = 2;  // a tile's start-up takes the time of two blocks
 constexpr int kThreads = 224;  // 4 softmax warps, key producer, MMA issuer, value producer
 constexpr uint32_t kBoxBytes = 64 * 128;  // 64 rows x 64 bf16
 constexpr int kKUnits = 3, kVUnits = 4;
@@ -48,7 +50,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct Params {
-  Shape shape;  // tile_rows = kTileRows
+  Shape shape;  // tile_rows = kTileRows, block_keys = kBlock
   Plan plan;
   int num_pages;
   const int32_t* page_table;

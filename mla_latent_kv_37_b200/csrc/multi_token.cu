@@ -42,9 +42,9 @@ int set_attributes() {
   std::lock_guard<std::mutex> lock(mu);
   if (done[dev]) return MLA_OK;
   if ((e = cudaFuncSetAttribute(simt::prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(simt::Layout<192, 128>::kBytes))) != cudaSuccess ||
+                                static_cast<int>(simt::PromptLayout::kBytes))) != cudaSuccess ||
       (e = cudaFuncSetAttribute(simt::chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(simt::Layout<576, 512>::kBytes))) != cudaSuccess)
+                                static_cast<int>(simt::ChunkLayout::kBytes))) != cudaSuccess)
     return host_cuda_error(e, "cudaFuncSetAttribute");
   if ((e = cudaFuncSetAttribute(prompt::prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(prompt::kSmemBytes))) != cudaSuccess)
@@ -64,7 +64,7 @@ struct ChunkSpace {
 ChunkSpace chunk_space(const mla_dims* d, int n_tokens, int num_splits, int sms) {
   ChunkSpace w{};
   const bool bf16 = d->dtype == MLA_BF16;
-  w.tile_rows = bf16 ? chunk::kTileRows : simt::kRows;
+  w.tile_rows = bf16 ? chunk::kTileRows : simt::ChunkLayout::kRows;
   w.parts = num_splits > 0 ? num_splits : bf16 ? sms / 2 : sms;  // CTA pairs, or CTAs
   const int64_t rows = static_cast<int64_t>(n_tokens) * d->n_heads;
   w.max_tiles = static_cast<int>(rows / w.tile_rows + std::min<int64_t>(d->batch, n_tokens));
@@ -183,9 +183,10 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
   if ((rc = host_device(&dev)) || (rc = set_attributes())) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const float scale_log2 = resolve_scale(softmax_scale) * kLog2e;
-  // every sequence has at most one tile that is not full
+  // every sequence has at most one tile that is not full, and every tile has a token
   const auto tiles = [&](int rows) {
-    return static_cast<unsigned>(n_tokens / rows + std::min(dims->batch, n_tokens));
+    return static_cast<unsigned>(std::min<int64_t>(
+        n_tokens, int64_t{n_tokens} / rows + std::min(dims->batch, n_tokens)));
   };
   if (dims->dtype == MLA_BF16) {
     // heads x tokens of 64-column boxes of 128 tokens; tokens past n_tokens read as zero
@@ -232,8 +233,8 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
   p.o = o;
   p.lse = lse;
   p.status = dev.status;
-  host_launch(simt::prompt_kernel, dim3(tiles(simt::kRows), dims->n_heads), dim3(simt::kThreads),
-              simt::Layout<192, 128>::kBytes, st, p);
+  host_launch(simt::prompt_kernel, dim3(tiles(simt::PromptLayout::kRows) * dims->n_heads),
+              dim3(simt::PromptLayout::kThreads), simt::PromptLayout::kBytes, st, p);
   return host_launched();
 }
 
@@ -273,8 +274,11 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  const chunk::Shape shape{n_tokens, dims->batch, dims->n_heads, max_pages,
-                           w.tile_rows, cu_tokens, seq_lens};
+  const bool bf16 = dims->dtype == MLA_BF16;
+  const chunk::Shape shape{n_tokens, dims->batch, dims->n_heads, max_pages, w.tile_rows,
+                           bf16 ? chunk::kBlock : simt::kChunkBlock,
+                           bf16 ? chunk::kBlockCost : simt::kChunkBlockCost,
+                           bf16 ? chunk::kSegCost : simt::kChunkSegCost, cu_tokens, seq_lens};
   const chunk::Plan plan{reinterpret_cast<int32_t*>(ws + w.plan), dims->batch, w.max_tiles,
                          w.parts};
   float* part_o = reinterpret_cast<float*>(ws + w.part_o);
@@ -283,7 +287,7 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
               dev.status);
   if ((rc = host_launched())) return rc;
   const float scale_log2 = resolve_scale(softmax_scale) * kLog2e;
-  if (dims->dtype == MLA_BF16) {
+  if (bf16) {
     // rows of 576 in boxes of 64 columns x 64 rows: the queries, and the pool's pages
     const auto map = [&](CUtensorMap* m, const void* base, int64_t rows) {
       const uint64_t dim[2] = {chunk::kRow, static_cast<uint64_t>(rows)};
@@ -303,8 +307,8 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
   } else {
     const simt::ChunkParams p{shape, plan, num_pages, q_cat, cache_pool, page_table, scale_log2,
                               o_lat, lse, part_o, part_lse, dev.status};
-    host_launch(simt::chunk_kernel, dim3(w.parts), dim3(simt::kThreads),
-                simt::Layout<576, 512>::kBytes, st, p);
+    host_launch(simt::chunk_kernel, dim3(w.parts), dim3(simt::ChunkLayout::kThreads),
+                simt::ChunkLayout::kBytes, st, p);
   }
   if ((rc = host_launched())) return rc;
   if (w.parts == 1) return MLA_OK;
