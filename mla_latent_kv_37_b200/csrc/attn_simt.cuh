@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(PromptLayout::kThreads, 2) prompt_kernel(const
 // ------------------------------------------------------------------------------------------
 struct ChunkParams {
   chunk::Shape shape;
-  chunk::Plan plan;
-  int num_pages;
+  int parts, num_pages;
+  chunk::PartStart* starts;
   const void* q_cat;
   const void* pool;
   const int32_t* page_table;
@@ -426,8 +426,10 @@ struct ChunkSrc {
 
 // 64 rows a block (their queries take 145 KB), and parts that end at any multiple of 16 keys: a
 // step of 64 keys takes about 18 us here, too long to be the grain of a small call.
-constexpr int kChunkWarps = 8, kChunkBlock = 16;
+constexpr int kChunkWarps = 8, kChunkTileShift = 6, kChunkBlockShift = 4;
+constexpr int kChunkBlock = 1 << kChunkBlockShift;
 using ChunkLayout = Layout<576, 512, kChunkWarps, 1>;
+static_assert(ChunkLayout::kRows == 1 << kChunkTileShift, "a tile's rows");
 // in the plan's units: a block of 16 keys (9000 clocks), and a start-up (query load, write-back)
 constexpr int kChunkBlockCost = 4, kChunkSegCost = 2;
 
@@ -436,10 +438,15 @@ __global__ void __launch_bounds__(ChunkLayout::kThreads, 1) chunk_kernel(const C
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.shape.n_heads;
-  chunk::SegIter it(p.shape, p.plan, blockIdx.x);
+  chunk::Place from{}, to{};
+  const bool any = chunk::find_part(p.shape, p.parts, blockIdx.x,
+                                    reinterpret_cast<chunk::Scratch*>(smem), p.status, from, to);
+  if (threadIdx.x == 0) chunk::write_start(p.shape, any, from, p.starts + blockIdx.x);
+  __syncthreads();
+  chunk::SegIter it(p.shape, any, from, to);
   chunk::Tile t;
-  int tile, b0, b1, blocks;
-  while (it.next(t, tile, b0, b1, blocks)) {
+  int b0, b1, blocks;
+  while (it.next(t, b0, b1, blocks)) {
     const int j0 = b0 * kChunkBlock;
     const int j1 = min(b1 * kChunkBlock, t.visible(t.rows - 1, H));
     const int64_t row0 = static_cast<int64_t>(t.tok0) * H + t.row0;

@@ -1,12 +1,15 @@
 // Work division of the attention of a chunk of new tokens over the paged latent cache.
 //
 // The query rows of a sequence, (token, head) pairs with the head running fastest, are cut into
-// tiles of `tile_rows` rows; a tile attends to the keys its last row sees.  The list of all
-// tiles' key blocks (block_keys keys each) is cut into `parts` ranges of equal cost, one for each
+// tiles of 2^tile_shift rows; a tile attends to the keys its last row sees.  The list of all
+// tiles' key blocks (2^block_shift keys each) is cut into `parts` ranges of equal cost, one for each
 // resident CTA (pair): few rows over long caches spread over the machine (split-KV), many rows
 // stay whole.  A range may end inside a tile; the parts of such a tile write normalised partial
-// results with their log-sum-exp, which combine_kernel merges in the order of the parts, so the
+// results with their log-sum-exp, which a second kernel merges in the order of the parts, so the
 // result does not depend on timing.
+//
+// Every block of the attention kernel finds its own range, a tile a thread and two passes where the
+// tiles are more than the threads: a kernel of its own for the plan took 6 us before the first load.
 //
 // Cost of a tile, in units of the kernel's choice: its start-up (query load, drained pipeline,
 // write-back) and its key blocks.
@@ -18,28 +21,11 @@ namespace mla {
 namespace chunk {
 
 constexpr int kPage = 64, kRow = 576, kDc = 512;
-constexpr int kPlanThreads = 1024;
-
-// Plan in the workspace, written by plan_kernel.
-struct Plan {
-  int32_t* base;
-  int B, max_tiles, max_parts;
-  __host__ __device__ static size_t words(int64_t B, int64_t max_tiles, int64_t max_parts) {
-    return static_cast<size_t>(4 + 2 * (max_tiles + 1) + (B + 1) + max_tiles + 2 * (max_parts + 1));
-  }
-  __host__ __device__ int32_t* header() const { return base; }  // tiles, parts
-  // virtual start of each tile (int64), then one past the last
-  __host__ __device__ int64_t* vstart() const { return reinterpret_cast<int64_t*>(base + 4); }
-  __host__ __device__ int32_t* seq_tile() const { return base + 4 + 2 * (max_tiles + 1); }
-  __host__ __device__ int32_t* tile_seq() const { return seq_tile() + B + 1; }
-  __host__ __device__ int32_t* part_tile() const { return tile_seq() + max_tiles; }
-  __host__ __device__ int32_t* part_block() const { return part_tile() + max_parts + 1; }
-};
-
-// What a plan is made for.
+// What the work is.
 struct Shape {
-  int n_tokens, batch, n_heads, max_pages, tile_rows;
-  int block_keys, block_cost, seg_cost;
+  int n_tokens, batch, n_heads, max_pages;
+  int tile_shift, block_shift;  // 2^ rows of a tile, keys of a block
+  int block_cost, seg_cost;
   const int32_t* cu;
   const int32_t* seq_lens;
 };
@@ -57,23 +43,40 @@ struct Tile {
     return min(max(first + (row0 + r) / n_heads + 1, 0), len);
   }
   __device__ int blocks(const Shape& s) const {
-    return (visible(rows - 1, s.n_heads) + s.block_keys - 1) / s.block_keys;
+    return (visible(rows - 1, s.n_heads) + (1 << s.block_shift) - 1) >> s.block_shift;
   }
 };
-__device__ __forceinline__ Tile tile_at(const Shape& s, const Plan& plan, int i) {
+// Tiles of a sequence, and its k-th one.
+__device__ __forceinline__ int tiles_of(const Shape& s, int tokens) {
+  const int64_t rows = static_cast<int64_t>(tokens) * s.n_heads;
+  return static_cast<int>((rows + (1 << s.tile_shift) - 1) >> s.tile_shift);
+}
+__device__ __forceinline__ Tile tile_at(const Shape& s, int seq, int k) {
   Tile t;
-  t.seq = plan.tile_seq()[i];
-  const packed::Span sp = packed::span(s.cu, t.seq, s.n_tokens);
-  t.row0 = (i - plan.seq_tile()[t.seq]) * s.tile_rows;
-  t.rows = min(s.tile_rows, sp.size() * s.n_heads - t.row0);
+  t.seq = seq;
+  const packed::Span sp = packed::span(s.cu, seq, s.n_tokens);
+  t.row0 = k << s.tile_shift;
+  t.rows = min(1 << s.tile_shift, sp.size() * s.n_heads - t.row0);
   t.tok0 = sp.begin;
-  t.len = clamped_len(s, t.seq);
+  t.len = clamped_len(s, seq);
   t.first = t.len - sp.size();
   return t;
 }
 
-__device__ inline int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// A place in the list of blocks: block `block` of tile `k` of sequence `seq`, tile `index` of all.
+struct Place {
+  int seq, k, block, index;
+};
+// Where a part begins, for the merge: index < 0 if it has nothing.  row: the first of the tile's
+// rows among all (token, head) rows.
+struct PartStart {
+  int32_t index, block, rows, pad;
+  int64_t row, pad2;
+};
+
+// Exclusive sum over the block's threads (whole warps, at most 32).
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -82,130 +85,172 @@ __device__ inline int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* tot
   }
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
-  if (w == 0) {
-    int64_t s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
+  int64_t before = x - v, sum = 0;
+  for (int i = 0; i < warps; ++i) {
+    const int64_t y = warp_sums[i];
+    if (i < w) before += y;
+    sum += y;
   }
   __syncthreads();
-  const int64_t before = (w > 0 ? warp_sums[w - 1] : 0) + x - v;
-  *total = warp_sums[31];
-  __syncthreads();
+  *total = sum;
   return before;
 }
 
-// One block.  Tiles per sequence and their prefix, each tile's sequence and virtual start, and
-// the place (tile, block) where each part begins.
-__global__ void __launch_bounds__(kPlanThreads)
-    plan_kernel(const Shape s, Plan plan, int parts_req, unsigned int* status) {
-  __shared__ int64_t warp_sums[32];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int T = kPlanThreads, tid = threadIdx.x;
-  const int64_t max_tiles = plan.max_tiles, least = s.seg_cost + s.block_cost;
-  int64_t total;
-  int n_tiles = 0;
+constexpr int kMaxPlanThreads = 256;
+
+// Scratch in shared memory of find_part.
+struct Scratch {
+  int64_t warp_sums[32];
+  Place found[2];
+  int first[kMaxPlanThreads], size[kMaxPlanThreads], len[kMaxPlanThreads];  // of a round of
+                                                                            // sequences
+};
+
+// The range [from, to) of part `part` of `parts`; false if it is empty.  All threads of the block.
+__device__ inline bool find_part(const Shape& s, int parts, int part, Scratch* sc,
+                                 unsigned int* status, Place& from, Place& to) {
+  const int T = blockDim.x, tid = threadIdx.x;
   bool bad = false;
-  for (int b0 = 0; b0 < s.batch; b0 += T) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < s.batch) {
-      const int64_t rows =
-          static_cast<int64_t>(packed::span(s.cu, b, s.n_tokens, &bad).size()) * s.n_heads;
-      n = static_cast<int>((rows + s.tile_rows - 1) / s.tile_rows);
-      const int len = s.seq_lens[b];
-      bad |= len < 0 || len > s.max_pages * kPage;
-    }
-    const int64_t at = block_scan(n, warp_sums, &total) + n_tiles;
-    if (b < s.batch) plan.seq_tile()[b] = static_cast<int>(min(at, max_tiles));
-    // (spans that overlap, which only a malformed cu has, could need more tiles than there are)
-    n_tiles = static_cast<int>(min(n_tiles + total, max_tiles));
-  }
-  if (bad) atomicOr(status, MLA_STATUS_BAD_LENGTH);
-  if (tid == 0) plan.seq_tile()[s.batch] = n_tiles;
-  __syncthreads();
-  // each tile's sequence: the last one that starts at or before it and is not empty
-  int64_t v = 0;
-  for (int i0 = 0; i0 < n_tiles; i0 += T) {
-    const int i = i0 + tid;
-    int64_t cost = 0;
-    if (i < n_tiles) {
-      int lo = 0, hi = s.batch;  // seq_tile[lo] <= i < seq_tile[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (plan.seq_tile()[mid] <= i) lo = mid; else hi = mid;
+  // f(place of a tile, its cost or 0 without a tile), a round of T tiles at a time
+  const auto each_round = [&](auto&& f) {
+    int base = 0;
+    for (int b0 = 0; b0 < s.batch; b0 += T) {
+      const int b = b0 + tid;
+      int size = 0, n = 0;
+      if (b < s.batch) {
+        const int len = s.seq_lens[b];
+        size = packed::span(s.cu, b, s.n_tokens, &bad).size();
+        n = tiles_of(s, size);
+        sc->len[tid] = min(max(len, 0), s.max_pages * kPage);
+        bad |= len < 0 || len > s.max_pages * kPage;
       }
-      plan.tile_seq()[i] = lo;
-      cost = s.seg_cost + static_cast<int64_t>(s.block_cost) * tile_at(s, plan, i).blocks(s);
+      sc->size[tid] = size;
+      int64_t total;
+      sc->first[tid] = static_cast<int>(block_scan(n, sc->warp_sums, &total));
+      __syncthreads();
+      const int tiles = static_cast<int>(total);
+      for (int i0 = 0; i0 < tiles; i0 += T) {
+        const int i = i0 + tid;
+        Place at{0, 0, 0, base + i};
+        int64_t cost = 0;
+        if (i < tiles) {
+          int lo = 0, hi = T;  // the last sequence that begins at or before tile i is not empty
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sc->first[mid] <= i) lo = mid; else hi = mid;
+          }
+          at.seq = b0 + lo;
+          at.k = i - sc->first[lo];
+          Tile t;
+          t.row0 = at.k << s.tile_shift;
+          t.rows = min(1 << s.tile_shift, sc->size[lo] * s.n_heads - t.row0);
+          t.len = sc->len[lo];
+          t.first = t.len - sc->size[lo];
+          cost = s.seg_cost + static_cast<int64_t>(s.block_cost) * t.blocks(s);
+        }
+        f(at, cost);
+      }
+      __syncthreads();
+      base += tiles;
     }
-    const int64_t at = block_scan(cost, warp_sums, &total) + v;
-    if (i < n_tiles) plan.vstart()[i] = at;
-    v += total;
-  }
-  if (tid == 0) plan.vstart()[n_tiles] = v;
+  };
+  int rounds = 0;
+  int64_t V = 0, mine_v = 0, mine_cost = 0;
+  Place mine{};
+  each_round([&](const Place& at, int64_t cost) {
+    int64_t total;
+    mine = at;
+    mine_cost = cost;
+    mine_v = block_scan(cost, sc->warp_sums, &total) + V;
+    V += total;
+    ++rounds;
+  });
+  if (bad && part == 0) atomicOr(status, MLA_STATUS_BAD_LENGTH);
+  // part c begins at place floor(c V / C).  No part is worth less than a start-up or a block (but
+  // for a lone one), so no two begin at the same block past a tile's first.
+  const int least = max(s.seg_cost, s.block_cost);
+  const int C = V >= static_cast<int64_t>(parts) * least ? parts
+                                                         : max(static_cast<int>(V) / least, V > 0);
+  if (part >= C) return false;
+  const bool small = V <= 0xffffffffll;  // (a 64-bit division takes a few hundred clocks)
+  const int64_t q = small ? static_cast<uint32_t>(V) / static_cast<uint32_t>(C) : V / C;
+  const uint32_t rest = static_cast<uint32_t>(V - q * C);  // c rest / C: c, rest < C <= 65536
+  const auto begin = [&](uint32_t c) { return c * q + c * rest / static_cast<uint32_t>(C); };
+  const int64_t u[2] = {begin(part), part + 1 == C ? V : begin(part + 1)};
+  const auto locate = [&](const Place& at, int64_t v0, int64_t cost) {  // (cost 0: no tile)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (v0 <= u[e] && u[e] < v0 + cost) {
+        sc->found[e] = at;
+        if (u[e] - v0 > s.seg_cost)
+          sc->found[e].block = static_cast<int>((u[e] - v0 - s.seg_cost) / s.block_cost);
+      }
+  };
+  if (tid == 0) sc->found[1] = Place{s.batch, 0, 0, 0x7fffffff};  // behind the last tile
   __syncthreads();
-  // part c begins at virtual place floor(c V / C).  No part is worth less than a start-up and a
-  // block, so no two of them begin at the same block.
-  const int64_t V = v;
-  const int64_t most = V / least;
-  const int C = most < 1 ? 1 : most < parts_req ? static_cast<int>(most) : parts_req;
-  for (int i = tid; i < n_tiles; i += T) {
-    const int64_t v0 = plan.vstart()[i], v1 = plan.vstart()[i + 1];
-    for (int64_t c = (v0 * C + V - 1) / V; c < C; ++c) {
-      const int64_t u = c * V / C;
-      if (u >= v1) break;
-      if (u < v0) continue;
-      plan.part_tile()[c] = i;
-      plan.part_block()[c] =
-          u - v0 > s.seg_cost ? static_cast<int>((u - v0 - s.seg_cost) / s.block_cost) : 0;
-    }
+  if (rounds == 1) {
+    locate(mine, mine_v, mine_cost);
+  } else {
+    int64_t before = 0;
+    each_round([&](const Place& at, int64_t cost) {
+      int64_t total;
+      const int64_t v0 = block_scan(cost, sc->warp_sums, &total) + before;
+      before += total;
+      locate(at, v0, cost);
+    });
   }
-  for (int c = tid; c <= plan.max_parts; c += T)
-    if (c >= (n_tiles > 0 ? C : 0)) {
-      plan.part_tile()[c] = n_tiles;
-      plan.part_block()[c] = 0;
-    }
-  if (tid == 0) {
-    plan.header()[0] = n_tiles;
-    plan.header()[1] = n_tiles > 0 ? C : 0;
-  }
+  __syncthreads();
+  from = sc->found[0];
+  to = sc->found[1];
+  return true;
 }
 
-// The segments of part c: whole tiles, but for a first one that begins and a last one that ends
+// The segments of a range: whole tiles, but for a first one that begins and a last one that ends
 // inside its tile.  Tiles without a visible key come as segments of no blocks.
 struct SegIter {
   const Shape* s;
-  Plan plan;
-  int i, b, i_end, b_end;  // next (tile, block), and where the part ends
-  __device__ SegIter(const Shape& shape, const Plan& p, int c) : s(&shape), plan(p) {
-    const bool in = c < p.header()[1];
-    i = in ? p.part_tile()[c] : 0;
-    b = in ? p.part_block()[c] : 0;
-    i_end = in ? p.part_tile()[c + 1] : 0;
-    b_end = in ? p.part_block()[c + 1] : 0;
-  }
-  __device__ bool next(Tile& t, int& tile, int& b0, int& b1, int& blocks) {
-    if (i > i_end || (i == i_end && b >= b_end)) return false;
-    tile = i;
-    t = tile_at(*s, plan, i);
+  Place at, to;
+  __device__ SegIter(const Shape& shape, bool any, const Place& from, const Place& end)
+      : s(&shape), at(from), to(any ? end : from) {}
+  __device__ bool next(Tile& t, int& b0, int& b1, int& blocks) {
+    if (at.seq > to.seq || (at.seq == to.seq && (at.k > to.k || (at.k == to.k && at.block >= to.block))))
+      return false;
+    const auto tiles = [&]() { return tiles_of(*s, packed::span(s->cu, at.seq, s->n_tokens).size()); };
+    while (at.k >= tiles()) {  // the next sequence that has tiles
+      if (++at.seq > to.seq || at.seq >= s->batch) return false;
+      at.k = 0;
+    }
+    const bool last = at.seq == to.seq && at.k == to.k;
+    if (at.seq == to.seq && (at.k > to.k || (last && at.block >= to.block))) return false;
+    t = tile_at(*s, at.seq, at.k);
     blocks = t.blocks(*s);
-    b0 = b;
-    b1 = i < i_end ? blocks : b_end;
-    ++i;
-    b = 0;
+    b0 = at.block;
+    b1 = last ? to.block : blocks;
+    ++at.k;
+    at.block = 0;
     return true;
   }
 };
 
+// The merge's record of a part, by one thread.
+__device__ __forceinline__ void write_start(const Shape& s, bool any, const Place& from,
+                                            PartStart* out) {
+  PartStart r{-1, 0, 0, 0, 0, 0};
+  if (any) {
+    const Tile t = tile_at(s, from.seq, from.k);
+    r = PartStart{from.index, from.block, t.rows, 0,
+                  static_cast<int64_t>(t.tok0) * s.n_heads + t.row0, 0};
+  }
+  *out = r;
+}
+
 // Partial results: part c's tile that it enters in the middle goes to slot 2c, the one that it
-// begins and does not finish to slot 2c + 1.  part_o [2 C][tile_rows][512], part_lse alike.
+// begins and does not finish to slot 2c + 1.  part_lse [2 C][tile_rows]; part_o [2 C][tile_rows][512],
+// or, where a thread has a row (kByColumn), [2 C][128][tile_rows][4], so that the threads of a warp
+// write 512 bytes side by side.
 __device__ __forceinline__ int partial_slot(int c, int b0) { return 2 * c + (b0 == 0 ? 1 : 0); }
 
-constexpr int kCombineWarps = 8;
+constexpr int kCombineThreads = 256;
 
 template <typename O> __device__ __forceinline__ void store4(O* p, float4 v);
 template <> __device__ __forceinline__ void store4<float>(float* p, float4 v) {
@@ -215,29 +260,38 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16*
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// grid (parts - 1, tile_rows / kCombineWarps): the boundary of parts x and x + 1, if it is the
-// first one inside its tile.  One warp per row; lane l holds columns 4 (l + 32 k) ... + 3.
+// The parts of the boundary of parts c - 1 and c, if it is the first one inside its tile: the slots
+// are 2 (c - 1) + 1, then 2 k for k = c ... last.
+__device__ __forceinline__ bool split_tile(const PartStart* starts, int parts, int c, PartStart& r,
+                                           int& last) {
+  r = starts[c];
+  const PartStart before = starts[c - 1];
+  if (r.index < 0 || r.block == 0 || (before.index == r.index && before.block > 0)) return false;
+  last = c;
+  while (last + 1 < parts && starts[last + 1].index == r.index && starts[last + 1].block > 0) ++last;
+  return true;
+}
+__device__ __forceinline__ int contributor(int k, int c) { return k < c ? 2 * k + 1 : 2 * k; }
+
+// Row-major partial results: grid (parts - 1, tile_rows / 8), one warp per row; lane l holds
+// columns 4 (l + 32 k) ... + 3.
 template <typename O>
-__global__ void __launch_bounds__(32 * kCombineWarps)
-    combine_kernel(const Shape s, Plan plan, const float* __restrict__ part_o,
-                   const float* __restrict__ part_lse, O* __restrict__ o, float* __restrict__ lse) {
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_rows_kernel(int parts, int tile_rows, const PartStart* __restrict__ starts,
+                        const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                        O* __restrict__ o, float* __restrict__ lse) {
   griddep_launch_dependents();
   griddep_wait();
-  const int C = plan.header()[1], c = blockIdx.x + 1;
-  if (c >= C || plan.part_block()[c] == 0) return;
-  const int i = plan.part_tile()[c];
-  if (plan.part_tile()[c - 1] == i && plan.part_block()[c - 1] > 0) return;  // not the first
-  const Tile t = tile_at(s, plan, i);
-  const int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int c = blockIdx.x + 1;
+  PartStart t;
+  int last;
+  if (!split_tile(starts, parts, c, t, last)) return;
+  const int r = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= t.rows) return;
   const float NEG_INF = -__int_as_float(0x7f800000);
-  // contributors: slot 2 (c - 1) + 1, then 2 k for k = c ... last
-  int last = c;
-  while (last + 1 < C && plan.part_tile()[last + 1] == i && plan.part_block()[last + 1] > 0) ++last;
-  const auto slot = [&](int k) { return k < c ? 2 * k + 1 : 2 * k; };
   float m = NEG_INF;
   for (int k = c - 1 + lane; k <= last; k += 32)
-    m = fmaxf(m, part_lse[static_cast<size_t>(slot(k)) * s.tile_rows + r]);
+    m = fmaxf(m, part_lse[static_cast<size_t>(contributor(k, c)) * tile_rows + r]);
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
   float tot = 0.f;
@@ -246,7 +300,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int k = c - 1; k <= last; ++k) {
-    const size_t at = static_cast<size_t>(slot(k)) * s.tile_rows + r;
+    const size_t at = static_cast<size_t>(contributor(k, c)) * tile_rows + r;
     const float l = part_lse[at];
     const float w = l == NEG_INF ? 0.f : expf(l - m);
     tot += w;
@@ -261,12 +315,70 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     }
   }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;  // (a NaN stays one)
-  const int64_t row = static_cast<int64_t>(t.tok0) * s.n_heads + t.row0 + r;
+  const int64_t row = t.row + r;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     store4(o + row * kDc + 4 * (lane + 32 * q),
            make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv));
   if (lane == 0 && lse) lse[row] = tot == 0.f ? NEG_INF : m + logf(tot);
+}
+
+// Partial results by column groups: grid (parts - 1, tile_rows / 32, 4), lane = row, warp w has the
+// columns 128 z + 4 (w + 8 k) ... + 3, k < 4.  The rows go out through shared memory.
+template <typename O>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_columns_kernel(int parts, int tile_rows, const PartStart* __restrict__ starts,
+                           const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                           O* __restrict__ o, float* __restrict__ lse) {
+  __shared__ float4 turn[32][33];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x + 1;
+  PartStart t;
+  int last;
+  if (!split_tile(starts, parts, c, t, last)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.y * 32, r = r0 + lane;
+  if (r0 >= t.rows) return;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const auto part_l = [&](int k) {
+    return part_lse[static_cast<size_t>(contributor(k, c)) * tile_rows + r];
+  };
+  float m = NEG_INF;  // (rows past the tile's last hold what the attention left there: -inf and 0)
+#pragma unroll 4
+  for (int k = c - 1; k <= last; ++k) m = fmaxf(m, part_l(k));
+  float tot = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = c - 1; k <= last; ++k) {
+    const float l = part_l(k), w = l == NEG_INF ? 0.f : expf(l - m);
+    tot += w;
+    const float4* src =
+        reinterpret_cast<const float4*>(part_o) +
+        (static_cast<size_t>(contributor(k, c)) * (kDc / 4) + 32 * blockIdx.z + warp) * tile_rows + r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 x = src[static_cast<size_t>(8 * q) * tile_rows];
+      acc[q].x += w * x.x;
+      acc[q].y += w * x.y;
+      acc[q].z += w * x.z;
+      acc[q].w += w * x.w;
+    }
+  }
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;  // (a NaN stays one)
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    turn[lane][warp + 8 * q] =
+        make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
+  __syncthreads();
+#pragma unroll
+  for (int i = warp; i < 32; i += kCombineThreads / 32)
+    if (r0 + i < t.rows)
+      store4(o + (t.row + r0 + i) * kDc + 128 * blockIdx.z + 4 * lane, turn[i][lane]);
+  if (blockIdx.z == 0 && warp == 0 && r < t.rows && lse)
+    lse[t.row + r] = tot == 0.f ? NEG_INF : m + logf(tot);
 }
 
 }  // namespace chunk

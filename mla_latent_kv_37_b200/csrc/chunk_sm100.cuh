@@ -31,8 +31,8 @@
 namespace mla {
 namespace chunk {
 
-constexpr int kTileRows = 128, kCtaRows = 64;
-constexpr int kBlock = 128;  // keys per block: two pages
+constexpr int kTileShift = 7, kTileRows = 1 << kTileShift, kCtaRows = 64;
+constexpr int kBlockShift = 7, kBlock = 1 << kBlockShift;  // keys per block: two pages
 constexpr int kBlockCost = 1, kSegCost = 2;  // a tile's start-up takes the time of two blocks
 constexpr int kThreads = 224;  // 4 softmax warps, key producer, MMA issuer, value producer
 constexpr uint32_t kBoxBytes = 64 * 128;  // 64 rows x 64 bf16
@@ -50,9 +50,9 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct Params {
-  Shape shape;  // tile_rows = kTileRows, block_keys = kBlock
-  Plan plan;
-  int num_pages;
+  Shape shape;
+  int parts, num_pages;
+  PartStart* starts;
   const int32_t* page_table;
   float scale_log2;
   void* o;
@@ -142,6 +142,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int part = blockIdx.x >> 1;
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_c);
+  }
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
@@ -183,16 +187,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   const int H = p.shape.n_heads;
-  SegIter it(p.shape, p.plan, part);
+  Place from{}, to{};
+  const bool any = find_part(p.shape, p.parts, part, reinterpret_cast<Scratch*>(smem + kOffP),
+                             p.status, from, to);
+  if (rank == 0 && threadIdx.x == 0) write_start(p.shape, any, from, p.starts + part);
+  __syncthreads();  // P's place held the scratch
+  SegIter it(p.shape, any, from, to);
   Tile t;
-  int tile, b0, b1, blocks;
+  int b0, b1, blocks;
 
   if (warp == 4 || warp == 6) {
     // =================== TMA producers: queries and keys (warp 4), values (warp 6) ============
     const bool keys = warp == 4;
     bool ok = true;
     int n = 0, sg = 0, tails = 0;  // blocks, non-empty segments, and ragged blocks so far
-    while (ok && it.next(t, tile, b0, b1, blocks)) {
+    while (ok && it.next(t, b0, b1, blocks)) {
       if (b0 == b1) continue;
       const int32_t* table = p.page_table + static_cast<int64_t>(t.seq) * p.shape.max_pages;
       const int pages = (t.visible(t.rows - 1, H) + kPage - 1) / kPage;
@@ -333,7 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
       int n = 0, sg = 0;  // S issued, non-empty segments begun
-      while (ok && it.next(t, tile, b0, b1, blocks)) {
+      while (ok && it.next(t, b0, b1, blocks)) {
         if (b0 == b1) continue;
         ok = warp_wait(&bars->q_full, sg & 1, wc);
         if (ok) issue_s(n, b0 + 1 == b1);
@@ -361,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // left alone at one of their barriers.
     bool ok = true;
     int n = 0;
-    while (it.next(t, tile, b0, b1, blocks)) {
+    while (it.next(t, b0, b1, blocks)) {
       const int vis = r < t.rows ? t.visible(r, H) : 0;
       float m_ref = NEG_INF, l_sum = 0.f;
       for (int b = b0; b < b1; ++b, ++n) {
@@ -448,9 +457,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // ---- O / l -> global ----
       const bool whole = b0 == 0 && b1 == blocks;
+      const int slot = partial_slot(part, b0);
       const int64_t out = whole ? static_cast<int64_t>(t.tok0) * H + t.row0 + r
-                                : static_cast<int64_t>(partial_slot(part, b0)) * kTileRows + r;
-      const bool in = r < t.rows;
+                                : static_cast<int64_t>(slot) * kTileRows + r;
+      const bool in = r < t.rows || !whole;  // (a partial result has all rows; the rest are zero)
       // the sums of the row's two halves; the block before last used the same places, and its
       // readers have passed a barrier since
       bars->xch[n & 1][L] = l_sum;
@@ -461,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (b1 > b0) ok = ok && warp_wait(&bars->pv_done, (n - 1) & 1, wc);
       if (!ok) continue;
       tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < 256; c += 32) {
         uint32_t x[32];
         __syncwarp();
@@ -487,10 +497,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             reinterpret_cast<uint4*>(d)[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          float* d = (whole ? static_cast<float*>(p.o) : p.part_o) + out * kDc + col;
+          // a row's columns, or its place among the rows of each group of four
+          float4* d = whole ? reinterpret_cast<float4*>(static_cast<float*>(p.o) + out * kDc + col)
+                            : reinterpret_cast<float4*>(p.part_o) +
+                                  (static_cast<int64_t>(slot) * (kDc / 4) + col / 4) * kTileRows + r;
+          const int step = whole ? 1 : kTileRows;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            reinterpret_cast<float4*>(d)[k] = make_float4(
+            d[k * step] = make_float4(
                 __uint_as_float(x[4 * k]) * inv, __uint_as_float(x[4 * k + 1]) * inv,
                 __uint_as_float(x[4 * k + 2]) * inv, __uint_as_float(x[4 * k + 3]) * inv);
         }

@@ -56,25 +56,23 @@ int set_attributes() {
   return MLA_OK;
 }
 
-// Workspace of mla_chunk_attn: plan, then the partial results of the parts.
+// Workspace of mla_chunk_attn: where the parts begin, and their partial results.
 struct ChunkSpace {
-  size_t plan, part_o, part_lse, total;
-  int tile_rows, max_tiles, parts;
+  size_t starts, part_o, part_lse, total;
+  int tile_rows, parts;
 };
-ChunkSpace chunk_space(const mla_dims* d, int n_tokens, int num_splits, int sms) {
+ChunkSpace chunk_space(const mla_dims* d, int num_splits, int sms) {
   ChunkSpace w{};
   const bool bf16 = d->dtype == MLA_BF16;
   w.tile_rows = bf16 ? chunk::kTileRows : simt::ChunkLayout::kRows;
   w.parts = num_splits > 0 ? num_splits : bf16 ? sms / 2 : sms;  // CTA pairs, or CTAs
-  const int64_t rows = static_cast<int64_t>(n_tokens) * d->n_heads;
-  w.max_tiles = static_cast<int>(rows / w.tile_rows + std::min<int64_t>(d->batch, n_tokens));
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = (off + bytes + 255) / 256 * 256;
     return o;
   };
-  w.plan = take(4 * chunk::Plan::words(d->batch, w.max_tiles, w.parts));
+  w.starts = take(sizeof(chunk::PartStart) * w.parts);
   w.part_o = take(2ull * w.parts * w.tile_rows * kDc * 4);
   w.part_lse = take(2ull * w.parts * w.tile_rows * 4);
   w.total = off;
@@ -244,7 +242,7 @@ size_t mla_chunk_workspace_size(const mla_dims* dims, int32_t n_tokens, int32_t 
     return 0;
   HostDevice dev{148, nullptr};
   (void)host_device(&dev);
-  return chunk_space(dims, n_tokens, num_splits, dev.sms).total;
+  return chunk_space(dims, num_splits, dev.sms).total;
 }
 
 int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tokens,
@@ -270,22 +268,19 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
   if (!aligned(workspace, 256)) return MLA_ERR_ALIGN;
   HostDevice dev;
   if ((rc = host_device(&dev)) || (rc = set_attributes())) return rc;
-  const ChunkSpace w = chunk_space(dims, n_tokens, num_splits, dev.sms);
+  const ChunkSpace w = chunk_space(dims, num_splits, dev.sms);
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   const bool bf16 = dims->dtype == MLA_BF16;
-  const chunk::Shape shape{n_tokens, dims->batch, dims->n_heads, max_pages, w.tile_rows,
-                           bf16 ? chunk::kBlock : simt::kChunkBlock,
+  const chunk::Shape shape{n_tokens, dims->batch, dims->n_heads, max_pages,
+                           bf16 ? chunk::kTileShift : simt::kChunkTileShift,
+                           bf16 ? chunk::kBlockShift : simt::kChunkBlockShift,
                            bf16 ? chunk::kBlockCost : simt::kChunkBlockCost,
                            bf16 ? chunk::kSegCost : simt::kChunkSegCost, cu_tokens, seq_lens};
-  const chunk::Plan plan{reinterpret_cast<int32_t*>(ws + w.plan), dims->batch, w.max_tiles,
-                         w.parts};
+  chunk::PartStart* starts = reinterpret_cast<chunk::PartStart*>(ws + w.starts);
   float* part_o = reinterpret_cast<float*>(ws + w.part_o);
   float* part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-  host_launch(chunk::plan_kernel, dim3(1), dim3(chunk::kPlanThreads), 0, st, shape, plan, w.parts,
-              dev.status);
-  if ((rc = host_launched())) return rc;
   const float scale_log2 = resolve_scale(softmax_scale) * kLog2e;
   if (bf16) {
     // rows of 576 in boxes of 64 columns x 64 rows: the queries, and the pool's pages
@@ -300,26 +295,29 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
     if ((rc = map(&tq, q_cat, static_cast<int64_t>(n_tokens) * dims->n_heads)) ||
         (rc = map(&tc, cache_pool, static_cast<int64_t>(num_pages) * kPageN)))
       return rc;
-    const chunk::Params p{shape, plan, num_pages, page_table, scale_log2, o_lat,
+    const chunk::Params p{shape, w.parts, num_pages, starts, page_table, scale_log2, o_lat,
                           o_dtype == MLA_FP32, lse, part_o, part_lse, dev.status, host_wait_ns()};
     host_launch(chunk::pair_kernel, dim3(2 * w.parts), dim3(chunk::kThreads), chunk::kSmemBytes,
                 st, tq, tc, p);
   } else {
-    const simt::ChunkParams p{shape, plan, num_pages, q_cat, cache_pool, page_table, scale_log2,
+    const simt::ChunkParams p{shape, w.parts, num_pages, starts, q_cat, cache_pool, page_table, scale_log2,
                               o_lat, lse, part_o, part_lse, dev.status};
     host_launch(simt::chunk_kernel, dim3(w.parts), dim3(simt::ChunkLayout::kThreads),
                 simt::ChunkLayout::kBytes, st, p);
   }
   if ((rc = host_launched())) return rc;
   if (w.parts == 1) return MLA_OK;
-  const dim3 grid(w.parts - 1, w.tile_rows / chunk::kCombineWarps);
-  const dim3 block(32 * chunk::kCombineWarps);
-  if (o_dtype == MLA_FP32)
-    host_launch(chunk::combine_kernel<float>, grid, block, 0, st, shape, plan, part_o, part_lse,
-                static_cast<float*>(o_lat), lse);
+  const dim3 block(chunk::kCombineThreads);
+  if (!bf16)
+    host_launch(chunk::combine_rows_kernel<float>, dim3(w.parts - 1, w.tile_rows / 8), block, 0, st,
+                w.parts, w.tile_rows, starts, part_o, part_lse, static_cast<float*>(o_lat), lse);
+  else if (o_dtype == MLA_FP32)
+    host_launch(chunk::combine_columns_kernel<float>, dim3(w.parts - 1, w.tile_rows / 32, 4), block, 0,
+                st, w.parts, w.tile_rows, starts, part_o, part_lse, static_cast<float*>(o_lat), lse);
   else
-    host_launch(chunk::combine_kernel<__nv_bfloat16>, grid, block, 0, st, shape, plan, part_o,
-                part_lse, static_cast<__nv_bfloat16*>(o_lat), lse);
+    host_launch(chunk::combine_columns_kernel<__nv_bfloat16>,
+                dim3(w.parts - 1, w.tile_rows / 32, 4), block, 0, st, w.parts, w.tile_rows, starts,
+                part_o, part_lse, static_cast<__nv_bfloat16*>(o_lat), lse);
   return host_launched();
 }
 

@@ -8,7 +8,7 @@
 // the sum need no exchange), the other's products do.  Order of the products:
 //   PV0(j) S0(j+1) PV1(j) S1(j+1) PV0(j+1) ...
 //   * TMEM (512 columns): S0 | S1 | O0 | O1, 128 each.  P (bf16) overwrites the first half of its
-//     own S and is the A operand of PV from there.
+//     own S and is the A operand of PV from there, half by half.
 //   * Shared memory: the queries 96 KB, a ring of four 16 KB key boxes (128 keys x 64 columns;
 //     three make a key tile, released one by one) and two 32 KB value tiles.
 //   * The running maximum is a reference that moves only when it would grow by more than 2^8, so O
@@ -61,7 +61,8 @@ struct Bars {
   uint64_t v_full[kVSlots];   // TMA: a value tile landed (bytes)
   uint64_t v_empty[kVSlots];  // MMA: both tiles' PV have read it (commit)
   uint64_t s_full[2];         // MMA: a tile's S is written (commit)
-  uint64_t p_full[2];         // the tile's four softmax warps: P written, O rescaled (4)
+  uint64_t p_half[2];         // the tile's four softmax warps: P of 64 keys written, O rescaled (4)
+  uint64_t p_full[2];         // the same: all of P written (4)
   uint64_t o_full[2];         // MMA: the tile's last PV is done (commit)
   uint64_t drain;
   uint32_t tmem_base;
@@ -92,6 +93,7 @@ __global__ void __maxnreg__(168)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_half[i], 4);
       mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->o_full[i], 1);
     }
@@ -209,23 +211,26 @@ __global__ void __maxnreg__(168)
       const bool first = t == 0 || j >= n0, last = t == 1 || j >= n1;
       const int s = j % kVSlots;
       if (first) ok = ok && warp_wait(&bars->v_full[s], (j / kVSlots) & 1, wc);
-      ok = ok && warp_wait(&bars->p_full[t], j & 1, wc);
-      if (!ok) return;
-      tc_fence_after();
       const int steps = (min(kTile, len - j * kTile) + 15) / 16;
-      if (elect_one()) {
-        const uint64_t b = at(d_v, 2 * s * kBox);
-        const uint32_t o = tmem + kTmemO + 128 * t, a = tmem + kTmemS + kTile * t;
-        if (steps == kTile / 16) {
+      const uint64_t b = at(d_v, 2 * s * kBox);
+      const uint32_t o = tmem + kTmemO + 128 * t, a = tmem + kTmemS + kTile * t;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, j > 0 || k > 0);
-        } else {
-          for (int k = 0; k < steps; ++k)
-            mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, j > 0 || k > 0);
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && warp_wait(half ? &bars->p_full[t] : &bars->p_half[t], j & 1, wc);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          if (steps == kTile / 16) {
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, k > 0 || j > 0);
+          } else {
+            for (int k = 4 * half; k < min(4 * half + 4, steps); ++k)
+              mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, k > 0 || j > 0);
+          }
+          if (half && last) mma_commit(&bars->v_empty[s]);
+          if (half && j == (t ? n1 : n0) - 1) mma_commit(&bars->o_full[t]);
         }
-        if (last) mma_commit(&bars->v_empty[s]);
-        if (j == (t ? n1 : n0) - 1) mma_commit(&bars->o_full[t]);
       }
     };
     issue_s(0, 0);
@@ -295,6 +300,19 @@ __global__ void __maxnreg__(168)
         }
         l_sum *= alpha;
       }
+      // values past the sequence's end, among the last 16 keys that PV reads
+      const int valid = len - j * kTile;
+      if (valid < kTile && (valid & 15)) {
+        const int sv = j % kVSlots;
+        if (!(ok = warp_wait(&bars->v_full[sv], (j / kVSlots) & 1, wc))) break;
+        const int end = (valid + 15) & ~15;
+        if (r >= valid && r < end)
+          for (int c = 0; c < 2; ++c)
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(smem + kOffV + (2 * sv + c) * kBox + r * 128 + 16 * k) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
       const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-m_ref, -m_ref);
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -310,24 +328,11 @@ __global__ void __maxnreg__(168)
           pk[k] = pack_bf16x2(x0, x1);
         }
         tmem_st32(tS + 32 * c, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c ? &bars->p_full[t] : &bars->p_half[t]);
       }
-      // values past the sequence's end, among the last 16 keys that PV reads
-      const int valid = len - j * kTile;
-      if (valid < kTile && (valid & 15)) {
-        const int sv = j % kVSlots;
-        if (!(ok = warp_wait(&bars->v_full[sv], (j / kVSlots) & 1, wc))) break;
-        const int end = (valid + 15) & ~15;
-        if (r >= valid && r < end)
-          for (int c = 0; c < 2; ++c)
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(smem + kOffV + (2 * sv + c) * kBox + r * 128 + 16 * k) =
-                  make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_full[t]);
       float a0, a1;
       f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
       l_sum += a0 + a1;

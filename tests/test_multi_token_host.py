@@ -122,7 +122,7 @@ def test_chunk_splits_types_and_workspace(M):
     assert M.mla_chunk_workspace_size(d, 8, 65537) == 0
     assert M.mla_chunk_workspace_size(_d(M, d_c=1), 8) == 0
     assert M.mla_chunk_workspace_size(d, -1) == 0
-    sizes = [M.mla_chunk_workspace_size(d, n, s) for n, s in ((1, 1), (1, 8), (5000, 8), (5000, 200))]
+    sizes = [M.mla_chunk_workspace_size(d, n, s) for n, s in ((1, 1), (1, 8), (5000, 9), (5000, 200))]
     assert sizes == sorted(sizes) and len(set(sizes)) == 4 and all(s % 256 == 0 for s in sizes)
     if torch.cuda.is_available():
         assert _chunk(M, d, bytes=M.mla_chunk_workspace_size(d, 8) - 1) == -4
