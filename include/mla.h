@@ -305,7 +305,7 @@ int mla_out_proj_fp8(const mla_dims* dims, const float* o_lat, const void* w_uv,
  * Packed batches.  The new tokens of all sequences lie one behind the other: sequence b's are
  * tokens [cu_tokens[b], cu_tokens[b + 1]) of n_tokens, cu_tokens [batch + 1] int32 on the device,
  * cu_tokens[0] = 0, not decreasing, cu_tokens[batch] <= n_tokens.  A sequence may have none.
- * Tokens behind the last sequence are neither read nor written.  A cu_tokens that decreases or
+ * Tokens behind the last sequence have no influence and are not written.  A cu_tokens that decreases or
  * passes n_tokens raises MLA_STATUS_BAD_LENGTH and gives undefined results for the sequences it
  * damages, without an access out of range.
  * seq_lens[b] counts the sequence's rows with its new tokens: token i of n_b is row

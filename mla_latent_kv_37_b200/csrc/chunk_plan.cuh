@@ -25,7 +25,7 @@ constexpr int kPage = 64, kRow = 576, kDc = 512;
 struct Shape {
   int n_tokens, batch, n_heads, max_pages;
   int tile_shift, block_shift;  // 2^ rows of a tile, keys of a block
-  int block_cost, seg_cost;
+  int block_cost, seg_cost, least;  // least: no part is worth less (but for a lone one)
   const int32_t* cu;
   const int32_t* seq_lens;
 };
@@ -166,11 +166,11 @@ __device__ inline bool find_part(const Shape& s, int parts, int part, Scratch* s
     ++rounds;
   });
   if (bad && part == 0) atomicOr(status, MLA_STATUS_BAD_LENGTH);
-  // part c begins at place floor(c V / C).  No part is worth less than a start-up or a block (but
-  // for a lone one), so no two begin at the same block past a tile's first.
-  const int least = max(s.seg_cost, s.block_cost);
-  const int C = V >= static_cast<int64_t>(parts) * least ? parts
-                                                         : max(static_cast<int>(V) / least, V > 0);
+  // part c begins at place floor(c V / C).  least >= block_cost, so no two begin at the same block
+  // past a tile's first.
+  const int C = V >= static_cast<int64_t>(parts) * s.least
+                    ? parts
+                    : max(static_cast<int>(V) / s.least, V > 0);
   if (part >= C) return false;
   const bool small = V <= 0xffffffffll;  // (a 64-bit division takes a few hundred clocks)
   const int64_t q = small ? static_cast<uint32_t>(V) / static_cast<uint32_t>(C) : V / C;

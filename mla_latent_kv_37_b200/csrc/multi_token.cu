@@ -142,14 +142,13 @@ int mla_append_rows(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_to
   p.q_head = q_head_stride;
   p.qo_tok = q_out_token_stride;
   p.qo_head = q_out_head_stride;
-  p.theta = dims->rope_theta;
+  rope_frequencies(dims->rope_theta, p.inv_freq);
   p.status = dev.status;
-  p.heads_per_block = 16;
   const unsigned blocks = (static_cast<unsigned>(n_tokens) + rows::kTokens - 1) / rows::kTokens;
-  const unsigned slices =
-      q_rope ? (dims->n_heads + p.heads_per_block - 1) / p.heads_per_block : 0;
-  host_launch(dims->dtype == MLA_BF16 ? rows::append_rows_kernel<__nv_bfloat16>
-                                      : rows::append_rows_kernel<float>,
+  const bool bf16 = dims->dtype == MLA_BF16;
+  const int heads = bf16 ? rows::Chunk<__nv_bfloat16>::kHeads : rows::Chunk<float>::kHeads;
+  const unsigned slices = q_rope ? (dims->n_heads + heads - 1) / heads : 0;
+  host_launch(bf16 ? rows::append_rows_kernel<__nv_bfloat16> : rows::append_rows_kernel<float>,
               dim3(blocks, 1 + slices), dim3(rows::kThreads), 0,
               reinterpret_cast<cudaStream_t>(stream), p);
   return host_launched();
@@ -277,7 +276,8 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
                            bf16 ? chunk::kTileShift : simt::kChunkTileShift,
                            bf16 ? chunk::kBlockShift : simt::kChunkBlockShift,
                            bf16 ? chunk::kBlockCost : simt::kChunkBlockCost,
-                           bf16 ? chunk::kSegCost : simt::kChunkSegCost, cu_tokens, seq_lens};
+                           bf16 ? chunk::kSegCost : simt::kChunkSegCost,
+                           bf16 ? chunk::kLeast : simt::kChunkLeast, cu_tokens, seq_lens};
   chunk::PartStart* starts = reinterpret_cast<chunk::PartStart*>(ws + w.starts);
   float* part_o = reinterpret_cast<float*>(ws + w.part_o);
   float* part_lse = reinterpret_cast<float*>(ws + w.part_lse);

@@ -3,7 +3,9 @@
 // p = seq_lens[b] - n_b + i for token i of sequence b's n_b, R(p) the interleaved-pair rotation.
 //
 // Bound by HBM: a token's row is read and written once, 2 (576 + 64 H) elements in all, with 6
-// flops per rotated pair.
+// flops per rotated pair.  A thread's loads (eight chunks of 16 bytes of the queries) are on their
+// way before the block looks up its tokens' places and angles, which takes as long; the frequencies
+// come from the host, since a double-precision pow per block took longer than the loads.
 #pragma once
 #include "packed.cuh"
 #include "ptx_sm100.cuh"
@@ -17,7 +19,7 @@ constexpr int kTokens = kThreads / 32;  // a warp finds one token's place and 32
 constexpr int kDc = 512, kDr = 64, kRow = 576, kPage = 64;
 
 struct Params {
-  int n_tokens, batch, n_heads, max_pages, num_pages, heads_per_block;
+  int n_tokens, batch, n_heads, max_pages, num_pages;
   const int32_t* cu;
   const int32_t* seq_lens;
   const int32_t* page_table;
@@ -28,14 +30,14 @@ struct Params {
   void* k_rope;
   void* q_out;
   int64_t c_stride, kr_stride, q_tok, q_head, qo_tok, qo_head;  // elements
-  float theta;
+  double inv_freq[32];  // theta^(-2 pair / 64)
   unsigned int* status;
 };
 
 // 16 bytes of elements: 8 bf16 or 4 fp32, an even number of them, so pairs never straddle.
 template <typename T> struct Chunk;
 template <> struct Chunk<float> {
-  static constexpr int kN = 4;
+  static constexpr int kN = 4, kHeads = kThreads / (kDr / kN);  // heads of a block
   static __device__ __forceinline__ uint4 rotate(uint4 v, const float2* cs) {
     const float a = __uint_as_float(v.x), b = __uint_as_float(v.y);
     const float c = __uint_as_float(v.z), d = __uint_as_float(v.w);
@@ -46,7 +48,7 @@ template <> struct Chunk<float> {
   }
 };
 template <> struct Chunk<__nv_bfloat16> {
-  static constexpr int kN = 8;
+  static constexpr int kN = 8, kHeads = kThreads / (kDr / kN);
   // rotated in fp32 and rounded once to the storage type
   static __device__ __forceinline__ uint32_t pair(uint32_t v, float2 cs) {
     const float a = __uint_as_float(v << 16), b = __uint_as_float(v & 0xffff0000u);
@@ -60,14 +62,40 @@ template <> struct Chunk<__nv_bfloat16> {
 // grid (ceil(n_tokens / kTokens), 1 + head slices): block (x, 0) writes the cache rows of its
 // tokens, block (x, 1 + y) rotates their queries of slice y.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ Params p) {
   constexpr int kN = Chunk<T>::kN, kPairs = kN / 2, kRotChunks = kDr / kN, kLatChunks = kDc / kN;
+  constexpr int kRowChunks = kLatChunks + kRotChunks;
+  constexpr int kLoads = (kTokens * kRowChunks + kThreads - 1) / kThreads;  // 3 or 5
+  static_assert(kLoads <= kTokens, "both kinds of blocks load into the same registers");
   __shared__ float2 cs[kTokens][kDr / 2];
   __shared__ int64_t slot[kTokens];  // pool row, or -1: the token is skipped
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * kTokens;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = blockIdx.x * kTokens, n_here = min(kTokens, p.n_tokens - t0);
+  const bool rows = blockIdx.y == 0;
   griddep_launch_dependents();
   griddep_wait();
+  uint4 v[kTokens];
+  // queries: thread = (head, chunk), one token a load
+  const int h = (static_cast<int>(blockIdx.y) - 1) * Chunk<T>::kHeads + tid / kRotChunks;
+  const int r = tid % kRotChunks;
+  if (rows) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = tid + u * kThreads, k = i / kRowChunks, c = i % kRowChunks;
+      const int64_t t = t0 + k;
+      if (k < n_here)
+        v[u] = c < kLatChunks
+                   ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.c_kv) +
+                                                          t * p.c_stride) + c)
+                   : __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_r) +
+                                                          t * p.kr_stride) + (c - kLatChunks));
+    }
+  } else if (h < p.n_heads) {
+    const T* src = static_cast<const T*>(p.q) + t0 * p.q_tok + h * p.q_head + r * kN;
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u)
+      if (u < n_here) v[u] = *reinterpret_cast<const uint4*>(src + u * p.q_tok);
+  }
   {
     const int t = t0 + warp;
     int64_t s = -1;
@@ -88,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const Params p) {
               err = MLA_STATUS_BAD_PAGE;
             else
               s = static_cast<int64_t>(page) * kPage + pos % kPage;
-            cs[warp][lane] = rope_cs(p.theta, lane, static_cast<int>(pos));
+            cs[warp][lane] = rope_cs(p.inv_freq[lane], static_cast<int>(pos));
           }
         }
         if (err && lane == 0) atomicOr(p.status, err);
@@ -97,38 +125,26 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const Params p) {
     if (lane == 0) slot[warp] = s;
   }
   __syncthreads();
-  const int n_here = min(kTokens, p.n_tokens - t0);
-  if (blockIdx.y == 0) {
-    for (int i = threadIdx.x; i < n_here * (kLatChunks + kRotChunks); i += kThreads) {
-      const int k = i / (kLatChunks + kRotChunks), c = i % (kLatChunks + kRotChunks);
-      const int64_t t = t0 + k, s = slot[k];
-      if (s < 0) continue;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.pool) + s * kRow) + c;
-      if (c < kLatChunks) {
-        *dst = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.c_kv) +
-                                                    t * p.c_stride) + c);
-      } else {
-        const int r = c - kLatChunks;
-        const uint4 v = Chunk<T>::rotate(
-            __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_r) + t * p.kr_stride) +
-                  r),
-            &cs[k][r * kPairs]);
-        *dst = v;
-        if (p.k_rope) reinterpret_cast<uint4*>(static_cast<T*>(p.k_rope) + t * kDr)[r] = v;
+  if (rows) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = tid + u * kThreads, k = i / kRowChunks, c = i % kRowChunks;
+      if (k >= n_here || slot[k] < 0) continue;
+      uint4 x = v[u];
+      if (c >= kLatChunks) {
+        const int j = c - kLatChunks;
+        x = Chunk<T>::rotate(x, &cs[k][j * kPairs]);
+        if (p.k_rope)
+          reinterpret_cast<uint4*>(static_cast<T*>(p.k_rope) + static_cast<int64_t>(t0 + k) * kDr)[j] = x;
       }
+      reinterpret_cast<uint4*>(static_cast<T*>(p.pool) + slot[k] * kRow)[c] = x;
     }
-    return;
-  }
-  const int h0 = (blockIdx.y - 1) * p.heads_per_block;
-  const int per = min(p.heads_per_block, p.n_heads - h0) * kRotChunks;
-  for (int i = threadIdx.x; i < n_here * per; i += kThreads) {
-    const int k = i / per, c = i % per, h = h0 + c / kRotChunks, r = c % kRotChunks;
-    if (slot[k] < 0) continue;
-    const int64_t t = t0 + k;
-    const uint4 v = *(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + t * p.q_tok +
-                                                     h * p.q_head) + r);
-    reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + t * p.qo_tok + h * p.qo_head)[r] =
-        Chunk<T>::rotate(v, &cs[k][r * kPairs]);
+  } else if (h < p.n_heads) {
+    T* dst = static_cast<T*>(p.q_out) + t0 * p.qo_tok + h * p.qo_head + r * kN;
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u)
+      if (u < n_here && slot[u] >= 0)
+        *reinterpret_cast<uint4*>(dst + u * p.qo_tok) = Chunk<T>::rotate(v[u], &cs[u][r * kPairs]);
   }
 }
 
