@@ -325,35 +325,35 @@ def _rows_at(t, name, dtype, shape, dev):
     """Address and row stride of [T, width], whose rows are contiguous; the stride is the library's
     to check.  Where a dimension has one element, torch's stride says nothing: the distance that a
     contiguous tensor would have stands in."""
-    s0, s1 = t.stride() if t.dim() == 2 else (0, 0)
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
-            (s1 == 1 or not t.numel())):
-        _refuse(t, name, dtype, shape, dev)
-    return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        s0, s1 = t.stride()
+        if s1 == 1 or not t.numel():
+            return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+    _refuse(t, name, dtype, shape, dev)
 
 
 def _heads_at(t, name, dtype, shape, dev):
     """The same of [T, heads, width]: address, token stride, head stride."""
-    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
-            (s2 == 1 or not t.numel())):
-        _refuse(t, name, dtype, shape, dev)
-    n, h, w = shape
-    if h == 1:
-        s1 = w
-    return t.data_ptr(), s0 if n > 1 else max(w, h * s1), s1
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        s0, s1, s2 = t.stride()
+        if s2 == 1 or not t.numel():
+            n, h, w = shape
+            if h == 1:
+                s1 = w
+            return t.data_ptr(), s0 if n > 1 else max(w, h * s1), s1
+    _refuse(t, name, dtype, shape, dev)
 
 
 def _pool_at(t, dtype, dev):
     shape = t.shape
-    if t.dim() != 3:
+    if len(shape) != 3:
         raise ValueError(f"cache_pool must have shape (num_pages, 64, 576), got {tuple(shape)}")
     return _at(t, "cache_pool", dtype, (shape[0], 64, 576), dev), shape[0]
 
 
 def _table_at(t, batch, dev):
     shape = t.shape
-    if t.dim() != 2:
+    if len(shape) != 2:
         raise ValueError(f"page_table must have shape ({batch}, max_pages), got {tuple(shape)}")
     return _at(t, "page_table", torch.int32, (batch, shape[1]), dev), shape[1]
 
