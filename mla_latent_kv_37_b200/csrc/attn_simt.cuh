@@ -439,17 +439,16 @@ __global__ void __launch_bounds__(ChunkLayout::kThreads, 1) chunk_kernel(const C
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.shape.n_heads;
-  chunk::Place from{}, to{};
-  const bool any = chunk::find_part(p.shape, p.parts, blockIdx.x,
-                                    reinterpret_cast<chunk::Scratch*>(smem), p.status, from, to);
-  if (threadIdx.x == 0) chunk::write_start(p.shape, any, from, p.starts + blockIdx.x);
+  const chunk::Range range = chunk::find_part(p.shape, p.parts, blockIdx.x,
+                                              reinterpret_cast<chunk::Scratch*>(smem), p.status);
+  if (threadIdx.x == 0) chunk::write_start(p.shape, range, p.starts + blockIdx.x);
   __syncthreads();
-  chunk::SegIter it(p.shape, any, from, to);
-  chunk::Tile t;
-  int b0, b1, blocks;
-  while (it.next(t, b0, b1, blocks)) {
-    const int j0 = b0 * kChunkBlock;
-    const int j1 = min(b1 * kChunkBlock, t.visible(t.rows - 1, H));
+  chunk::SegIter it(p.shape, range);
+  chunk::Segment seg;
+  while (it.next(seg)) {
+    const chunk::Tile& t = seg.t;
+    const int j0 = seg.b0 * kChunkBlock;
+    const int j1 = min(seg.b1 * kChunkBlock, t.visible(t.rows - 1, H));
     const int64_t row0 = static_cast<int64_t>(t.tok0) * H + t.row0;
     const ChunkSrc src{static_cast<const float*>(p.q_cat) + row0 * chunk::kRow,
                        static_cast<const float*>(p.pool),
@@ -470,8 +469,8 @@ __global__ void __launch_bounds__(ChunkLayout::kThreads, 1) chunk_kernel(const C
         for (int k = 0; k < 16; ++k) o[i][k] = 0.f;
       }
     }
-    const bool whole = b0 == 0 && b1 == blocks;
-    const int slot = chunk::partial_slot(blockIdx.x, b0);
+    const bool whole = !seg.split;
+    const int slot = chunk::partial_slot(blockIdx.x, seg.inside);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 8 * warp + i;

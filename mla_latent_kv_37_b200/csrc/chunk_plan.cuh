@@ -8,6 +8,13 @@
 // results with their log-sum-exp, which a second kernel merges in the order of the parts, so the
 // result does not depend on timing.
 //
+// Teams.  Where all sequences have the same number w of tiles (a few proposed tokens each, the usual
+// case), w parts make a team that takes a range of (sequence, block) pairs together, part k of it
+// tile k: the tiles of a sequence then read the same keys at the same time, and the cache comes
+// from HBM once.  With ranges of one list of tiles they read them at w different times, and 32 x 4
+// tokens over 225 MB of rows read 779 MB.  Not for caches that stay in L2 anyway, nor where the
+// parts are not nearly a multiple of w.
+//
 // Every block of the attention kernel finds its own range, a tile a thread and two passes where the
 // tiles are more than the threads: a kernel of its own for the plan took 6 us before the first load.
 //
@@ -63,15 +70,22 @@ __device__ __forceinline__ Tile tile_at(const Shape& s, int seq, int k) {
   return t;
 }
 
-// A place in the list of blocks: block `block` of tile `k` of sequence `seq`, tile `index` of all.
+// A place in the list of blocks: block `block` of tile `k` of sequence `seq`, entry `index` of the
+// list of tiles (of teams: of sequences; k is the part's own).
 struct Place {
   int seq, k, block, index;
 };
+// A part's range [from, to), and the parts of its team.
+struct Range {
+  Place from, to;
+  int team;
+  bool any;
+};
 // Where a part begins, for the merge: index < 0 if it has nothing.  row: the first of the tile's
-// rows among all (token, head) rows.
+// rows among all (token, head) rows.  The range goes on in part + team.
 struct PartStart {
-  int32_t index, block, rows, pad;
-  int64_t row, pad2;
+  int32_t index, block, rows, team;
+  int64_t row, pad;
 };
 
 // Exclusive sum over the block's threads (whole warps, at most 32).
@@ -106,12 +120,31 @@ struct Scratch {
                                                                             // sequences
 };
 
-// The range [from, to) of part `part` of `parts`; false if it is empty.  All threads of the block.
-__device__ inline bool find_part(const Shape& s, int parts, int part, Scratch* sc,
-                                 unsigned int* status, Place& from, Place& to) {
+// Caches of fewer rows stay in L2 (37 MB of 126) whatever the order.
+constexpr int64_t kTeamKeys = 32768;
+
+// The parts of a team (1: no teams).  All threads of the block.
+__device__ inline int team_size(const Shape& s, int parts, int64_t* warp_sums) {
+  const int w = tiles_of(s, packed::span(s.cu, 0, s.n_tokens).size());
+  if (w < 2 || parts / w * w * 16 < parts * 15) return 1;
+  int64_t keys = 0, total;
+  for (int b0 = 0; b0 < s.batch; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    const bool in = b < s.batch;
+    if (!__syncthreads_and(!in || tiles_of(s, packed::span(s.cu, b, s.n_tokens).size()) == w)) return 1;
+    if (in) keys += clamped_len(s, b);
+  }
+  block_scan(keys, warp_sums, &total);
+  return total >= kTeamKeys ? w : 1;
+}
+
+// The range of part `part` of `parts`.  All threads of the block.
+__device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* sc,
+                                  unsigned int* status) {
   const int T = blockDim.x, tid = threadIdx.x;
   bool bad = false;
-  // f(place of a tile, its cost or 0 without a tile), a round of T tiles at a time
+  const int w = team_size(s, parts, sc->warp_sums), rank = part / w, ranks = parts / w;
+  // f(place of an entry, its cost or 0 without one), a round of T entries at a time
   const auto each_round = [&](auto&& f) {
     int base = 0;
     for (int b0 = 0; b0 < s.batch; b0 += T) {
@@ -120,7 +153,7 @@ __device__ inline bool find_part(const Shape& s, int parts, int part, Scratch* s
       if (b < s.batch) {
         const int len = s.seq_lens[b];
         size = packed::span(s.cu, b, s.n_tokens, &bad).size();
-        n = tiles_of(s, size);
+        n = w > 1 ? 1 : tiles_of(s, size);
         sc->len[tid] = min(max(len, 0), s.max_pages * kPage);
         bad |= len < 0 || len > s.max_pages * kPage;
       }
@@ -142,7 +175,7 @@ __device__ inline bool find_part(const Shape& s, int parts, int part, Scratch* s
           at.seq = b0 + lo;
           at.k = i - sc->first[lo];
           Tile t;
-          t.row0 = at.k << s.tile_shift;
+          t.row0 = (w > 1 ? w - 1 : at.k) << s.tile_shift;  // a team's last tile has the most keys
           t.rows = min(1 << s.tile_shift, sc->size[lo] * s.n_heads - t.row0);
           t.len = sc->len[lo];
           t.first = t.len - sc->size[lo];
@@ -168,15 +201,17 @@ __device__ inline bool find_part(const Shape& s, int parts, int part, Scratch* s
   if (bad && part == 0) atomicOr(status, MLA_STATUS_BAD_LENGTH);
   // part c begins at place floor(c V / C).  least >= block_cost, so no two begin at the same block
   // past a tile's first.
-  const int C = V >= static_cast<int64_t>(parts) * s.least
-                    ? parts
+  const int C = V >= static_cast<int64_t>(ranks) * s.least
+                    ? ranks
                     : max(static_cast<int>(V) / s.least, V > 0);
-  if (part >= C) return false;
+  Range r{};
+  r.team = w;
+  if (rank >= C) return r;
   const bool small = V <= 0xffffffffll;  // (a 64-bit division takes a few hundred clocks)
   const int64_t q = small ? static_cast<uint32_t>(V) / static_cast<uint32_t>(C) : V / C;
   const uint32_t rest = static_cast<uint32_t>(V - q * C);  // c rest / C: c, rest < C <= 65536
   const auto begin = [&](uint32_t c) { return c * q + c * rest / static_cast<uint32_t>(C); };
-  const int64_t u[2] = {begin(part), part + 1 == C ? V : begin(part + 1)};
+  const int64_t u[2] = {begin(rank), rank + 1 == C ? V : begin(rank + 1)};
   const auto locate = [&](const Place& at, int64_t v0, int64_t cost) {  // (cost 0: no tile)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -200,55 +235,74 @@ __device__ inline bool find_part(const Shape& s, int parts, int part, Scratch* s
     });
   }
   __syncthreads();
-  from = sc->found[0];
-  to = sc->found[1];
-  return true;
+  r.any = true;
+  r.from = sc->found[0];
+  r.to = sc->found[1];
+  if (w > 1) r.from.k = part % w;
+  return r;
 }
 
 // The segments of a range: whole tiles, but for a first one that begins and a last one that ends
 // inside its tile.  Tiles without a visible key come as segments of no blocks.
+struct Segment {
+  Tile t;
+  int b0, b1;   // blocks (of a team, only those that the tile has)
+  bool inside;  // begins inside its tile
+  bool split;   // begins or ends inside its tile
+};
 struct SegIter {
   const Shape* s;
   Place at, to;
-  __device__ SegIter(const Shape& shape, bool any, const Place& from, const Place& end)
-      : s(&shape), at(from), to(any ? end : from) {}
-  __device__ bool next(Tile& t, int& b0, int& b1, int& blocks) {
-    if (at.seq > to.seq || (at.seq == to.seq && (at.k > to.k || (at.k == to.k && at.block >= to.block))))
-      return false;
-    const auto tiles = [&]() { return tiles_of(*s, packed::span(s->cu, at.seq, s->n_tokens).size()); };
-    while (at.k >= tiles()) {  // the next sequence that has tiles
-      if (++at.seq > to.seq || at.seq >= s->batch) return false;
-      at.k = 0;
+  int team;
+  __device__ SegIter(const Shape& shape, const Range& r)
+      : s(&shape), at(r.from), to(r.any ? r.to : r.from), team(r.team) {}
+  __device__ __forceinline__ bool next(Segment& g) {
+    if (team > 1) {
+      if (at.seq > to.seq || (at.seq == to.seq && at.block >= to.block)) return false;
+    } else {
+      const auto behind = [&]() {
+        return at.seq > to.seq ||
+               (at.seq == to.seq && (at.k > to.k || (at.k == to.k && at.block >= to.block)));
+      };
+      if (behind()) return false;
+      while (at.k >= tiles_of(*s, packed::span(s->cu, at.seq, s->n_tokens).size())) {
+        if (++at.seq > to.seq || at.seq >= s->batch) return false;  // the next that has tiles
+        at.k = 0;
+      }
+      if (behind()) return false;
     }
-    const bool last = at.seq == to.seq && at.k == to.k;
-    if (at.seq == to.seq && (at.k > to.k || (last && at.block >= to.block))) return false;
-    t = tile_at(*s, at.seq, at.k);
-    blocks = t.blocks(*s);
-    b0 = at.block;
-    b1 = last ? to.block : blocks;
-    ++at.k;
+    const bool last = at.seq == to.seq && (team > 1 || at.k == to.k);
+    g.t = tile_at(*s, at.seq, at.k);
+    const int blocks = g.t.blocks(*s);
+    g.inside = at.block > 0;
+    g.split = g.inside || last;
+    g.b0 = min(at.block, blocks);
+    g.b1 = last ? min(to.block, blocks) : blocks;
+    if (team > 1) ++at.seq; else ++at.k;
     at.block = 0;
     return true;
   }
+  // The same as a call, for the warp that issues the products: with the search inlined there the
+  // compiler's code for the loop of products is slower (1024 tokens over 16384: 4.1 ms, not 3.7).
+  __device__ __noinline__ bool next_call(Segment& g) { return next(g); }
 };
 
 // The merge's record of a part, by one thread.
-__device__ __forceinline__ void write_start(const Shape& s, bool any, const Place& from,
-                                            PartStart* out) {
-  PartStart r{-1, 0, 0, 0, 0, 0};
-  if (any) {
-    const Tile t = tile_at(s, from.seq, from.k);
-    r = PartStart{from.index, from.block, t.rows, 0,
+__device__ __forceinline__ void write_start(const Shape& s, const Range& r, PartStart* out) {
+  PartStart p{-1, 0, 0, r.team, 0, 0};
+  if (r.any) {
+    const Tile t = tile_at(s, r.from.seq, r.from.k);
+    p = PartStart{r.from.index, r.from.block, t.rows, r.team,
                   static_cast<int64_t>(t.tok0) * s.n_heads + t.row0, 0};
   }
-  *out = r;
+  *out = p;
 }
 
 // Partial results: part c's tile that it enters in the middle goes to slot 2c, the one that it
 // begins and does not finish to slot 2c + 1.  part_lse [2 C][tile_rows]; part_o [2 C][tile_rows][512],
 // or, where a thread has a row (kByColumn), [2 C][128][tile_rows][4], so that the threads of a warp
 // write 512 bytes side by side.
-__device__ __forceinline__ int partial_slot(int c, int b0) { return 2 * c + (b0 == 0 ? 1 : 0); }
+__device__ __forceinline__ int partial_slot(int c, bool inside) { return 2 * c + (inside ? 0 : 1); }
 
 constexpr int kCombineThreads = 256;
 
@@ -260,18 +314,26 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16*
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// The parts of the boundary of parts c - 1 and c, if it is the first one inside its tile: the slots
-// are 2 (c - 1) + 1, then 2 k for k = c ... last.
-__device__ __forceinline__ bool split_tile(const PartStart* starts, int parts, int c, PartStart& r,
-                                           int& last) {
-  r = starts[c];
-  const PartStart before = starts[c - 1];
-  if (r.index < 0 || r.block == 0 || (before.index == r.index && before.block > 0)) return false;
-  last = c;
-  while (last + 1 < parts && starts[last + 1].index == r.index && starts[last + 1].block > 0) ++last;
-  return true;
-}
-__device__ __forceinline__ int contributor(int k, int c) { return k < c ? 2 * k + 1 : 2 * k; }
+// The parts of a tile that is split, where part c is the first that begins inside it: the slots are
+// 2 (c - team) + 1, then 2 k for k = c, c + team ... last.
+struct Split {
+  PartStart start;
+  int c, last, team;
+  __device__ bool find(const PartStart* starts, int parts, int part) {
+    start = starts[part];
+    c = last = part;
+    team = start.team;
+    if (start.index < 0 || start.block == 0) return false;
+    const PartStart before = starts[part - team];
+    if (before.index == start.index && before.block > 0) return false;
+    while (last + team < parts && starts[last + team].index == start.index &&
+           starts[last + team].block > 0)
+      last += team;
+    return true;
+  }
+  __device__ int count() const { return (last - c) / team + 2; }
+  __device__ int slot(int i) const { return i == 0 ? 2 * (c - team) + 1 : 2 * (c + (i - 1) * team); }
+};
 
 // Row-major partial results: grid (parts - 1, tile_rows / 8), one warp per row; lane l holds
 // columns 4 (l + 32 k) ... + 3.
@@ -282,16 +344,16 @@ __global__ void __launch_bounds__(kCombineThreads)
                         O* __restrict__ o, float* __restrict__ lse) {
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x + 1;
-  PartStart t;
-  int last;
-  if (!split_tile(starts, parts, c, t, last)) return;
+  Split sp;
+  if (!sp.find(starts, parts, blockIdx.x + 1)) return;
+  const PartStart& t = sp.start;
+  const int n = sp.count();
   const int r = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= t.rows) return;
   const float NEG_INF = -__int_as_float(0x7f800000);
   float m = NEG_INF;
-  for (int k = c - 1 + lane; k <= last; k += 32)
-    m = fmaxf(m, part_lse[static_cast<size_t>(contributor(k, c)) * tile_rows + r]);
+  for (int k = lane; k < n; k += 32)
+    m = fmaxf(m, part_lse[static_cast<size_t>(sp.slot(k)) * tile_rows + r]);
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
   float tot = 0.f;
@@ -299,8 +361,8 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = c - 1; k <= last; ++k) {
-    const size_t at = static_cast<size_t>(contributor(k, c)) * tile_rows + r;
+  for (int k = 0; k < n; ++k) {
+    const size_t at = static_cast<size_t>(sp.slot(k)) * tile_rows + r;
     const float l = part_lse[at];
     const float w = l == NEG_INF ? 0.f : expf(l - m);
     tot += w;
@@ -333,31 +395,31 @@ __global__ void __launch_bounds__(kCombineThreads)
   __shared__ float4 turn[32][33];
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x + 1;
-  PartStart t;
-  int last;
-  if (!split_tile(starts, parts, c, t, last)) return;
+  Split sp;
+  if (!sp.find(starts, parts, blockIdx.x + 1)) return;
+  const PartStart& t = sp.start;
+  const int n = sp.count();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = blockIdx.y * 32, r = r0 + lane;
   if (r0 >= t.rows) return;
   const float NEG_INF = -__int_as_float(0x7f800000);
   const auto part_l = [&](int k) {
-    return part_lse[static_cast<size_t>(contributor(k, c)) * tile_rows + r];
+    return part_lse[static_cast<size_t>(sp.slot(k)) * tile_rows + r];
   };
   float m = NEG_INF;  // (rows past the tile's last hold what the attention left there: -inf and 0)
 #pragma unroll 4
-  for (int k = c - 1; k <= last; ++k) m = fmaxf(m, part_l(k));
+  for (int k = 0; k < n; ++k) m = fmaxf(m, part_l(k));
   float tot = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = c - 1; k <= last; ++k) {
+  for (int k = 0; k < n; ++k) {
     const float l = part_l(k), w = l == NEG_INF ? 0.f : expf(l - m);
     tot += w;
     const float4* src =
         reinterpret_cast<const float4*>(part_o) +
-        (static_cast<size_t>(contributor(k, c)) * (kDc / 4) + 32 * blockIdx.z + warp) * tile_rows + r;
+        (static_cast<size_t>(sp.slot(k)) * (kDc / 4) + 32 * blockIdx.z + warp) * tile_rows + r;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float4 x = src[static_cast<size_t>(8 * q) * tile_rows];

@@ -189,21 +189,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   const int H = p.shape.n_heads;
-  Place from{}, to{};
-  const bool any = find_part(p.shape, p.parts, part, reinterpret_cast<Scratch*>(smem + kOffP),
-                             p.status, from, to);
-  if (rank == 0 && threadIdx.x == 0) write_start(p.shape, any, from, p.starts + part);
+  const Range range =
+      find_part(p.shape, p.parts, part, reinterpret_cast<Scratch*>(smem + kOffP), p.status);
+  if (rank == 0 && threadIdx.x == 0) write_start(p.shape, range, p.starts + part);
   __syncthreads();  // P's place held the scratch
-  SegIter it(p.shape, any, from, to);
-  Tile t;
-  int b0, b1, blocks;
+  SegIter it(p.shape, range);
+  Segment seg;
 
   if (warp == 4 || warp == 6) {
     // =================== TMA producers: queries and keys (warp 4), values (warp 6) ============
     const bool keys = warp == 4;
     bool ok = true;
     int n = 0, sg = 0, tails = 0;  // blocks, non-empty segments, and ragged blocks so far
-    while (ok && it.next(t, b0, b1, blocks)) {
+    while (ok && it.next(seg)) {
+      const Tile t = seg.t;
+      const int b0 = seg.b0, b1 = seg.b1;
       if (b0 == b1) continue;
       const int32_t* table = p.page_table + static_cast<int64_t>(t.seq) * p.shape.max_pages;
       const int pages = (t.visible(t.rows - 1, H) + kPage - 1) / kPage;
@@ -344,7 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
       int n = 0, sg = 0;  // S issued, non-empty segments begun
-      while (ok && it.next(t, b0, b1, blocks)) {
+      while (ok && it.next_call(seg)) {
+        const int b0 = seg.b0, b1 = seg.b1;
         if (b0 == b1) continue;
         ok = warp_wait(&bars->q_full, sg & 1, wc);
         if (ok) issue_s(n, b0 + 1 == b1);
@@ -372,7 +373,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // left alone at one of their barriers.
     bool ok = true;
     int n = 0;
-    while (it.next(t, b0, b1, blocks)) {
+    while (it.next(seg)) {
+      const Tile t = seg.t;
+      const int b0 = seg.b0, b1 = seg.b1;
       const int vis = r < t.rows ? t.visible(r, H) : 0;
       float m_ref = NEG_INF, l_sum = 0.f;
       for (int b = b0; b < b1; ++b, ++n) {
@@ -458,8 +461,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive_cluster(p_full);
       }
       // ---- O / l -> global ----
-      const bool whole = b0 == 0 && b1 == blocks;
-      const int slot = partial_slot(part, b0);
+      const bool whole = !seg.split;
+      const int slot = partial_slot(part, seg.inside);
       const int64_t out = whole ? static_cast<int64_t>(t.tok0) * H + t.row0 + r
                                 : static_cast<int64_t>(slot) * kTileRows + r;
       const bool in = r < t.rows || !whole;  // (a partial result has all rows; the rest are zero)

@@ -440,6 +440,30 @@ def test_chunk_long_context():
     c.check(o, l, every=37)
 
 
+@pytest.mark.parametrize("dtype", TYPES, **KW)
+@pytest.mark.parametrize("n,H,lens", [(4, 128, [2500, 2501, 9000, 7, 0, 20000, 3, 64]), (9, 16, [40000, 130, 128]),
+                                      (5, 48, [16500, 1, 16500, 5, 6]), (2, 96, [33000])],
+                         ids=lambda v: str(v) if isinstance(v, int) else "")
+def test_chunk_equal_counts_over_long_caches(dtype, n, H, lens):
+    # as many tiles in every sequence: teams of parts, ranges that end inside a sequence, tiles of one
+    # sequence that see different numbers of blocks, sequences without rows
+    c = Chunk(42, [n] * len(lens), lens, H, dtype, extra=1)
+    for splits in (0, 8, 16):
+        o, l, st = c.run(splits)
+        assert st == 0
+        c.check(o, l, every=3)
+        assert torch.all(o[-1] == 7.0) and torch.all(l[-1] == 7.0)
+
+
+def test_chunk_shared_pages():
+    # two sequences that begin alike share the pages of their beginning
+    c = Chunk(43, [3, 2], [500, 450], 64, torch.bfloat16)
+    c.cache.page_table[1, :4] = c.cache.page_table[0, :4]
+    o, l, st = c.run()
+    assert st == 0
+    c.check(o, l)
+
+
 def test_chunk_many_sequences():
     n = 1300
     tokens = [b % 3 for b in range(n)]
