@@ -66,6 +66,7 @@ struct Bars {
   uint64_t o_full[2];         // MMA: the tile's last PV is done (commit)
   uint64_t drain;
   uint32_t tmem_base;
+  int steps[2], len;          // key tiles of the two query tiles, tokens: for the MMA issuer
   int abort_flag;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
@@ -89,6 +90,12 @@ __global__ void __maxnreg__(168)
                                             index, count, sp, &bad);
   if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
   if (!there) return;  // the whole block
+  // the sequence's last rows first: they have the most keys
+  const int q0 = (count - 1 - index) * kRows, len = sp.size();
+  const int h = blockIdx.y, hk = h / (p.n_heads / p.n_kv_heads);
+  // key tiles of the two query tiles (the second may be empty); only the last one of all can hold
+  // keys past the sequence
+  const int n0 = q0 / kTile + 1, n1 = q0 + kTile < len ? n0 + 1 : 0, n_max = max(n0, n1);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
@@ -107,6 +114,9 @@ __global__ void __maxnreg__(168)
     }
     mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
+    bars->steps[0] = n0;
+    bars->steps[1] = n1;
+    bars->len = len;
     fence_mbar_init_cluster();
   }
   if (warp == 9) {
@@ -120,13 +130,6 @@ __global__ void __maxnreg__(168)
   const WaitCtx wc{&bars->abort_flag, p.status, p.wait_ns};
   volatile int never = 0;
   const WaitCtx drain_ctx{&never, p.status, kDrainNs};
-
-  // the sequence's last rows first: they have the most keys
-  const int q0 = (count - 1 - index) * kRows, len = sp.size();
-  const int h = blockIdx.y, hk = h / (p.n_heads / p.n_kv_heads);
-  // key tiles of the two query tiles (the second may be empty); only the last one of all can hold
-  // keys past the sequence
-  const int n0 = q0 / kTile + 1, n1 = q0 + kTile < len ? n0 + 1 : 0, n_max = max(n0, n1);
 
   if (warp == 8) {
     // =================== TMA producer ===================
@@ -181,6 +184,10 @@ __global__ void __maxnreg__(168)
       mbar_wait(&bars->v_full[i % kVSlots], (i / kVSlots) & 1, drain_ctx);
   } else if (warp == 9) {
     // =================== MMA issuer ===================
+    // (read back from shared memory: the compiler's code for the loop is 3% faster when it knows
+    // nothing of where the numbers come from)
+    const volatile Bars* vb = bars;
+    const int n0 = vb->steps[0], n1 = vb->steps[1], len = vb->len, n_max = max(n0, n1);
     const uint32_t id_s = idesc_bf16(kTile, kTile, 0, 0), id_o = idesc_bf16(kTile, 128, 0, 1);
     const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
     const uint64_t d_k = smem_desc(smem_u32(smem + kOffK), 16, 1024, kSwizzle128B);
