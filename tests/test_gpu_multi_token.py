@@ -144,6 +144,21 @@ def test_append_rows_many_sequences():
     _check_append(c, pool, k_rope, cat[..., 512:])
 
 
+@pytest.mark.parametrize("theta", [100.0, 500000.0])
+def test_append_rows_other_theta(theta):
+    import mla_latent_kv_37_b200 as M
+    c = Append(15, [3], [70001], 16, torch.float32)
+    d = M.dims(1, 16, dtype=torch.float32, rope_theta=theta)
+    k_rope = torch.empty(3, 64, device="cuda")
+    M.mla_append_rows(d, dev(c.ckr)[:, :512], dev(c.ckr)[:, 512:576], dev(_cu([3])),
+                      dev(torch.tensor([70001], dtype=torch.int32)), dev(c.cache.page_table),
+                      dev(c.cache.pool), k_rope=k_rope)
+    assert M.mla_get_status() == 0
+    for i in range(3):
+        c.close(k_rope[i].cpu(), O.rope(c.ckr[i, 512:576].double().numpy(), 69998 + i, theta),
+                c.ckr[i, 512:576])
+
+
 def test_append_rows_skips_what_has_no_slot():
     c = Append(14, [3, 2, 2], [100, 70, 5], 16, torch.bfloat16)
     table = c.cache.page_table.clone()
@@ -272,6 +287,42 @@ def test_prompt_large_logits(dtype):
             assert np.linalg.norm(to_np(o[:, h]) - ref) <= 7e-5 * np.linalg.norm(ref)
     else:
         c.check(o, None, heads=[0, 9])
+
+
+@pytest.mark.parametrize("dtype", TYPES, **KW)
+def test_prompt_nan_stays_with_what_it_enters(dtype):
+    c = Prompt(28, [200, 300], 16, 8, dtype)
+    a, la, _ = c.run()
+    c.q[250, 3, 100] = float("nan")
+    b, lb, st = c.run()
+    assert st == 0 and torch.isnan(b[250, 3]).all() and torch.isnan(lb[250, 3])
+    keep = torch.ones(c.T, 16, dtype=torch.bool)
+    keep[250, 3] = False
+    assert torch.equal(a[keep], b[keep]) and torch.equal(la[keep], lb[keep])
+    c.q[250, 3, 100] = 0
+    c.kv[400, 2, 7] = float("nan")  # a key of key head 2: rows from its own on, heads 4 and 5
+    b, lb, st = c.run()
+    hit = torch.zeros(c.T, 16, dtype=torch.bool)
+    hit[400:, 4:6] = True
+    assert torch.isnan(b[hit]).all() and torch.isnan(lb[hit]).all()
+    hit[250, 3] = True
+    assert torch.equal(a[~hit], b[~hit]) and torch.equal(la[~hit], lb[~hit])
+
+
+@pytest.mark.parametrize("dtype", TYPES, **KW)
+def test_prompt_many_sequences(dtype):
+    tokens = [(7 * b) % 13 for b in range(700)] + [260]
+    c = Prompt(29, tokens, 16, 4, dtype)
+    o, l, st = c.run()
+    assert st == 0
+    c.check(o, l, heads=[0, 13], seqs=[*range(0, 700, 37), 1, 2, 700])
+
+
+def test_prompt_long_fp32():
+    c = Prompt(30, [1500, 900], 16, 2, torch.float32)
+    o, l, st = c.run()
+    assert st == 0
+    c.check(o, l, heads=[0, 15])
 
 
 def test_prompt_long():
@@ -613,6 +664,51 @@ def test_graphs_streams_and_shared_workspace():
         o, l, _ = x.run()
         assert torch.equal(args[-1].cpu(), o)  # the query's sign flipped twice
         assert torch.equal(pargs[-1].cpu(), p.run()[0])
+
+
+def test_calls_on_two_streams_at_once():
+    import mla_latent_kv_37_b200 as M
+    c = Chunk(74, [40, 3], [3000, 2000], 128, torch.bfloat16)
+    p = Prompt(75, [700, 90], 32, 32, torch.bfloat16)
+    d, dp = M.dims(2, 128), M.dims(2, 32)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    args = [dev(c.q), dev(c.cache.pool), dev(c.cache.page_table), dev(_cu(c.tokens)),
+            dev(torch.tensor(c.lens, dtype=torch.int32))]
+    q, kv, kr, cu = dev(p.q), dev(p.kv), dev(p.kr[:, :64].contiguous()), dev(_cu(p.tokens))
+    outs = [torch.zeros(c.T, 128, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    po = torch.zeros(p.T, 32, 128, dtype=torch.bfloat16, device="cuda")
+    ws = [M.chunk_workspace(d, c.T) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            M.mla_chunk_attn(d, *args, outs[i], ws[i], stream=streams[i])  # without lse
+        M.mla_prompt_attn(dp, q, kv[..., :128], kr, kv[..., 128:], cu, po, stream=streams[2])
+    torch.cuda.synchronize()
+    assert M.mla_get_status() == 0
+    o, l, _ = c.run()
+    assert torch.equal(outs[0].cpu(), o) and torch.equal(outs[1].cpu(), o)
+    assert torch.equal(po.cpu(), p.run()[0])
+
+
+def test_waits_that_run_out_are_reported(monkeypatch):
+    # a limit of 1 ns ends every wait that does not succeed within its first tries: the kernels unwind,
+    # say so in the status word, and the next calls are as ever
+    c = Chunk(76, [5, 300, 1], [700, 900, 64], 48, torch.bfloat16)
+    p = Prompt(77, [300, 70, 1000], 16, 16, torch.bfloat16)
+    good, lse, st = c.run()
+    prompt = p.run()
+    assert st == 0 and prompt[2] == 0
+    monkeypatch.setenv("MLA_WAIT_NS", "1")
+    raised = 0
+    for _ in range(3):
+        raised |= c.run()[2]
+        raised |= p.run()[2]
+    assert raised == 0x4
+    monkeypatch.delenv("MLA_WAIT_NS")
+    o, l, st = c.run()
+    assert st == 0 and torch.equal(o, good) and torch.equal(l, lse)
+    again = p.run()
+    assert again[2] == 0 and torch.equal(again[0], prompt[0]) and torch.equal(again[1], prompt[1])
 
 
 def test_no_tokens_do_nothing():
