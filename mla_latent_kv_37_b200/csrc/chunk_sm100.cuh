@@ -88,48 +88,6 @@ struct ChunkBars {
 };
 static_assert(sizeof(ChunkBars) <= 1536, "barrier block");
 
-// --- two-SM forms -----------------------------------------------------------------------------
-__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrives on the barrier at this place in both CTAs once the tcgen05 work issued so far is done.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-// A TMA load into this CTA's shared memory that counts its bytes on the leader's barrier.
-__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* m, uint32_t leader_bar,
-                                             int32_t x, int32_t y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(leader_bar)
-      : "memory");
-}
-// Arrive at a barrier of either CTA.  What the arrival announces (P, cleared values) is written and
-// read in the arriving CTA's own shared memory, by its own tensor core, and fenced for it before;
-// so the order within the CTA is enough.  (A release for the cluster waits until all earlier
-// operations of the thread, copies too, are visible there: about 1200 clocks in the value
-// producer, 5.8 ms against 4.3 ms for 1024 tokens over 16384.)
-__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// Announces bytes to come; says nothing of what was done before.
-__device__ __forceinline__ void arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                   cluster_addr),
-               "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void pair_barrier(int id) {  // 64 threads: warps w and w ^ 2
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
@@ -172,11 +130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init_cluster();
   }
   if (warp == 5) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&bars->tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    pair_tmem_alloc(&bars->tmem_base, kTmemCols);
   }
   tc_fence_before();
   __syncthreads();
@@ -542,9 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   if (warp == 5) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(kTmemCols)
-                 : "memory");
+    pair_tmem_dealloc(tmem, kTmemCols);
   }
 }
 

@@ -9,6 +9,7 @@
 #include "chunk_plan.cuh"
 #include "chunk_sm100.cuh"
 #include "host_services.h"
+#include "prompt_pair_sm100.cuh"
 #include "prompt_sm100.cuh"
 #include "rows.cuh"
 
@@ -17,6 +18,10 @@ namespace {
 
 constexpr int kDc = 512, kDr = 64, kDn = 128, kDv = 128, kPageN = 64;
 constexpr int kMaxParts = 1 << 16;
+// Prompts of this many tokens on average run on pairs of SMs (64 heads, 8192 tokens in all: 4096 each
+// 713 us on pairs, 740 us without; 2048 each 445 and 436 us; 256 each 331 and 191 us, since a pair's
+// 512 rows fill badly).
+constexpr int kPairTokens = 4096;
 constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -49,6 +54,10 @@ int set_attributes() {
   if ((e = cudaFuncSetAttribute(prompt::prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(prompt::kSmemBytes))) != cudaSuccess)
     return host_cuda_error(e, "cudaFuncSetAttribute(prompt_kernel)");
+  if ((e = cudaFuncSetAttribute(prompt_pair::pair_kernel,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(prompt_pair::kSmemBytes))) != cudaSuccess)
+    return host_cuda_error(e, "cudaFuncSetAttribute(prompt_pair)");
   if ((e = cudaFuncSetAttribute(chunk::pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(chunk::kSmemBytes))) != cudaSuccess)
     return host_cuda_error(e, "cudaFuncSetAttribute(pair_kernel)");
@@ -186,27 +195,34 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
         n_tokens, int64_t{n_tokens} / rows + std::min(dims->batch, n_tokens)));
   };
   if (dims->dtype == MLA_BF16) {
-    // heads x tokens of 64-column boxes of 128 tokens; tokens past n_tokens read as zero
+    const bool pair = static_cast<int64_t>(n_tokens) >= int64_t{kPairTokens} * dims->batch;
+    // heads x tokens of 64-column boxes of 128 tokens (a CTA of a pair loads half of the keys); tokens
+    // past n_tokens read as zero
     const auto map = [&](CUtensorMap* m, const void* base, int width, int heads, int64_t head_stride,
-                         int64_t token_stride) {
+                         int64_t token_stride, uint32_t tokens) {
       const uint64_t dim[3] = {static_cast<uint64_t>(width), static_cast<uint64_t>(heads),
                                static_cast<uint64_t>(n_tokens)};
       const uint64_t str[2] = {2 * static_cast<uint64_t>(head_stride),
                                2 * static_cast<uint64_t>(token_stride)};
-      const uint32_t box[3] = {64, 1, prompt::kTile};
+      const uint32_t box[3] = {64, 1, tokens};
       return host_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dim, str, box,
                          CU_TENSOR_MAP_SWIZZLE_128B);
     };
+    const uint32_t keys = pair ? prompt::kTile / 2 : prompt::kTile;
     CUtensorMap tq, tk, tkr, tv;
-    if ((rc = map(&tq, q, kDn + kDr, dims->n_heads, q_head_stride, q_token_stride)) ||
-        (rc = map(&tk, k_nope, kDn, n_kv_heads, k_head_stride, k_token_stride)) ||
-        (rc = map(&tkr, k_rope, kDr, 1, k_rope_stride, k_rope_stride)) ||
-        (rc = map(&tv, v, kDv, n_kv_heads, v_head_stride, v_token_stride)))
+    if ((rc = map(&tq, q, kDn + kDr, dims->n_heads, q_head_stride, q_token_stride, prompt::kTile)) ||
+        (rc = map(&tk, k_nope, kDn, n_kv_heads, k_head_stride, k_token_stride, keys)) ||
+        (rc = map(&tkr, k_rope, kDr, 1, k_rope_stride, k_rope_stride, keys)) ||
+        (rc = map(&tv, v, kDv, n_kv_heads, v_head_stride, v_token_stride, prompt::kTile)))
       return rc;
     const prompt::Params p{n_tokens, dims->batch, dims->n_heads, n_kv_heads, cu_tokens, scale_log2,
                            static_cast<__nv_bfloat16*>(o), lse, dev.status, host_wait_ns()};
-    host_launch(prompt::prompt_kernel, dim3(tiles(prompt::kRows), dims->n_heads),
-                dim3(prompt::kThreads), prompt::kSmemBytes, st, tq, tk, tkr, tv, p);
+    if (pair)
+      host_launch(prompt_pair::pair_kernel, dim3(2 * tiles(prompt_pair::kRows), dims->n_heads),
+                  dim3(prompt_pair::kThreads), prompt_pair::kSmemBytes, st, tq, tk, tkr, tv, p);
+    else
+      host_launch(prompt::prompt_kernel, dim3(tiles(prompt::kRows), dims->n_heads),
+                  dim3(prompt::kThreads), prompt::kSmemBytes, st, tq, tk, tkr, tv, p);
     return host_launched();
   }
   simt::PromptParams p{};
