@@ -347,7 +347,8 @@ int mla_append_rows(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_to
  *   n_kv_heads divides n_heads (MLA_ERR_ARG); n_heads itself for MLA's up-projected keys.
  *   softmax_scale: 0 selects 1/sqrt(d_nope + d_rope).
  * No workspace.  The rows of one sequence never depend on another's, nor on what lies behind the
- * last one.
+ * last one.  Within a sequence, v has to be finite (a later token's value has weight zero, which
+ * does not silence a NaN); a NaN in q or k shows in the rows that see it and in no other.
  */
 int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
                     const int32_t* cu_tokens, const void* q, int64_t q_token_stride,
@@ -366,7 +367,8 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
  *   o_lat  [n_tokens, H, d_c] of type o_dtype: dims.dtype, or MLA_FP32 (for mla_out_proj and
  *          mla_merge_partials); on the bf16 path the weights p are rounded to bf16 either way.
  *   lse    [n_tokens, H] fp32, nullable.
- * What the pool holds behind a sequence's last row has no influence, whatever it is (NaN too).
+ * What the pool holds behind a sequence's last row has no influence, whatever it is (NaN too); the
+ * sequence's own rows have to be finite.
  * A token that sees no row (n_b > seq_lens[b]) gets o_lat = 0, lse = -inf.  Lengths outside
  * [0, max_pages * page_size] are clamped and raise MLA_STATUS_BAD_LENGTH, page ids out of range
  * read page 0 and raise MLA_STATUS_BAD_PAGE.
