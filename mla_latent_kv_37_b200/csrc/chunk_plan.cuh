@@ -319,16 +319,22 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16*
 struct Split {
   PartStart start;
   int c, last, team;
+  // One warp: a lane looks at one of the next 32 parts, since one after the other a dozen loads'
+  // latencies would add up.
   __device__ bool find(const PartStart* starts, int parts, int part) {
     start = starts[part];
     c = last = part;
     team = start.team;
     if (start.index < 0 || start.block == 0) return false;
-    const PartStart before = starts[part - team];
-    if (before.index == start.index && before.block > 0) return false;
-    while (last + team < parts && starts[last + team].index == start.index &&
-           starts[last + team].block > 0)
-      last += team;
+    const int lane = threadIdx.x & 31;
+    const auto inside = [&](int k) {
+      return k < parts && starts[k].index == start.index && starts[k].block > 0;
+    };
+    if (inside(part - team)) return false;
+    for (int n = 32; n == 32; last += n * team) {
+      const unsigned no = ~__ballot_sync(0xffffffffu, inside(last + (lane + 1) * team));
+      n = no ? __ffs(no) - 1 : 32;
+    }
     return true;
   }
   __device__ int count() const { return (last - c) / team + 2; }
