@@ -120,6 +120,8 @@ struct Scratch {
                                                                             // sequences
 };
 
+// A tile is split into about this many parts at most: the merge reads them one behind the other.
+constexpr int kMaxSplit = 24;
 // Caches of fewer rows stay in L2 (37 MB of 126) whatever the order.
 constexpr int64_t kTeamKeys = 32768;
 
@@ -144,7 +146,7 @@ __device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* 
   const int T = blockDim.x, tid = threadIdx.x;
   bool bad = false;
   const int w = team_size(s, parts, sc->warp_sums), rank = part / w, ranks = parts / w;
-  // f(place of an entry, its cost or 0 without one), a round of T entries at a time
+  // f(place of an entry, its cost or 0 without one), a round of T entries at a time; their number
   const auto each_round = [&](auto&& f) {
     int base = 0;
     for (int b0 = 0; b0 < s.batch; b0 += T) {
@@ -186,11 +188,12 @@ __device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* 
       __syncthreads();
       base += tiles;
     }
+    return base;
   };
   int rounds = 0;
   int64_t V = 0, mine_v = 0, mine_cost = 0;
   Place mine{};
-  each_round([&](const Place& at, int64_t cost) {
+  const int entries = each_round([&](const Place& at, int64_t cost) {
     int64_t total;
     mine = at;
     mine_cost = cost;
@@ -201,8 +204,9 @@ __device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* 
   if (bad && part == 0) atomicOr(status, MLA_STATUS_BAD_LENGTH);
   // part c begins at place floor(c V / C).  least >= block_cost, so no two begin at the same block
   // past a tile's first.
-  const int C = V >= static_cast<int64_t>(ranks) * s.least
-                    ? ranks
+  const int most = min(static_cast<int64_t>(ranks), kMaxSplit * static_cast<int64_t>(entries));
+  const int C = V >= static_cast<int64_t>(most) * s.least
+                    ? most
                     : max(static_cast<int>(V) / s.least, V > 0);
   Range r{};
   r.team = w;

@@ -19,7 +19,8 @@
 //   * Shared memory: Q 72 KB | keys 72 KB | values 64 KB | P 16 KB.
 //   * The four softmax warps: a thread has half of a row's 128 scores; the two threads of a row
 //     exchange their maxima through shared memory.
-//   * Order of the products: S(t+1) before O(t), so that a softmax has the time of both.
+//   * S and O are issued by two warps, each waiting for its own operands: the tensor core takes what
+//     comes, and neither's waits hold up the other.
 // Statistics and O are fp32; P is rounded to bf16 for the tensor core (the sum adds the unrounded
 // weights).  The running maximum is a reference that moves only when it would grow by more than
 // 2^8, so O is hardly ever rescaled.
@@ -40,7 +41,7 @@ constexpr int kBlockShift = 7, kBlock = 1 << kBlockShift;  // keys per block: tw
 // Costs in blocks: a segment's start and write-back take the time of about four.  Parts of at least
 // four: eight single tokens over 64 ... 3000 keys take 25 us, 27 us with parts of two.
 constexpr int kBlockCost = 1, kSegCost = 4, kLeast = 4;
-constexpr int kThreads = 224;  // 4 softmax warps, key producer, MMA issuer, value producer
+constexpr int kThreads = 256;  // 4 softmax warps, key producer, S issuer, value producer, O issuer
 constexpr uint32_t kBoxBytes = 64 * 128;  // 64 rows x 64 bf16
 constexpr int kKUnits = 3, kVUnits = 4;
 constexpr uint32_t kKUnit = 3 * kBoxBytes, kVUnit = 2 * kBoxBytes;
@@ -85,7 +86,7 @@ struct ChunkBars {
   uint64_t pv_done;           // O of the block is added, P is free (commit)
   uint64_t o_free;            // L: the softmax warps of both CTAs have drained O (8)
   uint64_t v_tail[kVUnits];   // a value unit with rows past the sequence's end landed (bytes)
-  uint64_t drain;
+  uint64_t drain;             // both issuers' products are done (2 commits)
   uint32_t tmem_base;
   int abort_flag;
   float xch[2][kTileRows];    // the two halves of a row exchange maxima (block parity) and sums
@@ -129,7 +130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bars->p_full, 8);
     mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->o_free, 8);
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, 2);
     bars->abort_flag = 0;
     fence_mbar_init_cluster();
   }
@@ -249,70 +250,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = 0; u < kVUnits; ++u) mbar_wait(&bars->v_empty[u], (n - 1) & 1, wc);
       }
     }
-  } else if (warp == 5) {
-    // =================== MMA issuer (the leader's) ===================
+  } else if (warp == 5 || warp == 7) {
+    // =================== MMA issuers (the leader's): S (warp 5), O (warp 7) ===================
     if (rank == 0) {
-      const uint32_t id_s = idesc_bf16(kTileRows, kBlock, 0, 0);
-      const uint32_t id_o = idesc_bf16(kTileRows, 256, 0, 1);
-      const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
-      const uint64_t d_k = smem_desc(smem_u32(smem + kOffK), 16, 1024, kSwizzle128B);
-      const uint64_t d_p = smem_desc(smem_u32(smem + kOffP), 16, 1024, kSwizzle128B);
-      const uint64_t d_v = smem_desc(smem_u32(smem + kOffV), kBoxBytes, 1024, kSwizzle128B);
       const auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
       bool ok = true;
-      const auto issue_s = [&](int n, bool last) {
-        if (n >= 2) ok = warp_wait<true>(&bars->s_free[n & 1], ((n >> 1) - 1) & 1, wc);
+      int n = 0, sg = 0;  // blocks and non-empty segments so far
+      if (warp == 5) {
+        const uint32_t id_s = idesc_bf16(kTileRows, kBlock, 0, 0);
+        const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
+        const uint64_t d_k = smem_desc(smem_u32(smem + kOffK), 16, 1024, kSwizzle128B);
+        while (ok && it.next(seg)) {
+          const int b0 = seg.b0, b1 = seg.b1;
+          if (b0 == b1) continue;
+          ok = warp_wait(&bars->q_full, sg & 1, wc);
+          for (int b = b0; ok && b < b1; ++b, ++n) {
+            if (n >= 2) ok = warp_wait<true>(&bars->s_free[n & 1], ((n >> 1) - 1) & 1, wc);
 #pragma unroll
-        for (int u = 0; u < kKUnits; ++u) {
-          ok = ok && warp_wait(&bars->k_full[u], n & 1, wc);
-          if (!ok) return;
-          tc_fence_after();
-          if (elect_one()) {
+            for (int u = 0; u < kKUnits; ++u) {
+              ok = ok && warp_wait(&bars->k_full[u], n & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
+                for (int c = 0; c < 3; ++c)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                pair_mma_ss(tmem + kTmemS + 64 * (n & 1),
-                            at(d_q, (3 * u + c) * kBoxBytes + 32 * k),
-                            at(d_k, u * kKUnit + c * kBoxBytes + 32 * k), id_s,
-                            u > 0 || c > 0 || k > 0);
-            pair_commit(&bars->k_empty[u]);
-            if (u == kKUnits - 1) {
-              pair_commit(&bars->s_full[n & 1]);
-              if (last) pair_commit(&bars->q_empty);
+                  for (int k = 0; k < 4; ++k)
+                    pair_mma_ss(tmem + kTmemS + 64 * (n & 1),
+                                at(d_q, (3 * u + c) * kBoxBytes + 32 * k),
+                                at(d_k, u * kKUnit + c * kBoxBytes + 32 * k), id_s,
+                                u > 0 || c > 0 || k > 0);
+                pair_commit(&bars->k_empty[u]);
+                if (u == kKUnits - 1) {
+                  pair_commit(&bars->s_full[n & 1]);
+                  if (b + 1 == b1) pair_commit(&bars->q_empty);
+                }
+              }
             }
           }
+          ++sg;
         }
-      };
-      const auto issue_o = [&](int n, bool first) {
-        ok = ok && warp_wait<true>(&bars->p_full, n & 1, wc);
+      } else {
+        const uint32_t id_o = idesc_bf16(kTileRows, 256, 0, 1);
+        const uint64_t d_p = smem_desc(smem_u32(smem + kOffP), 16, 1024, kSwizzle128B);
+        const uint64_t d_v = smem_desc(smem_u32(smem + kOffV), kBoxBytes, 1024, kSwizzle128B);
+        while (ok && it.next(seg)) {
+          const int b0 = seg.b0, b1 = seg.b1;
+          if (b0 == b1) continue;
+          if (sg > 0) ok = warp_wait<true>(&bars->o_free, (sg - 1) & 1, wc);
+          for (int b = b0; ok && b < b1; ++b, ++n) {
+            ok = warp_wait<true>(&bars->p_full, n & 1, wc);
 #pragma unroll
-        for (int u = 0; u < kVUnits; ++u) {
-          ok = ok && warp_wait<true>(&bars->v_full[u], n & 1, wc);
-          if (!ok) return;
-          tc_fence_after();
-          if (elect_one()) {
+            for (int u = 0; u < kVUnits; ++u) {
+              ok = ok && warp_wait<true>(&bars->v_full[u], n & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pair_mma_ss(tmem + kTmemO + 128 * (u & 1), at(d_p, (u >> 1) * kBoxBytes + 32 * k),
-                          at(d_v, u * kVUnit + 2048 * k), id_o, u > 1 || k > 0 || !first);
-            pair_commit(&bars->v_empty[u]);
-            if (u == kVUnits - 1) pair_commit(&bars->pv_done);
+                for (int k = 0; k < 4; ++k)
+                  pair_mma_ss(tmem + kTmemO + 128 * (u & 1), at(d_p, (u >> 1) * kBoxBytes + 32 * k),
+                              at(d_v, u * kVUnit + 2048 * k), id_o, u > 1 || k > 0 || b > b0);
+                pair_commit(&bars->v_empty[u]);
+                if (u == kVUnits - 1) pair_commit(&bars->pv_done);
+              }
+            }
           }
+          ++sg;
         }
-      };
-      int n = 0, sg = 0;  // S issued, non-empty segments begun
-      while (ok && it.next_call(seg)) {
-        const int b0 = seg.b0, b1 = seg.b1;
-        if (b0 == b1) continue;
-        ok = warp_wait(&bars->q_full, sg & 1, wc);
-        if (ok) issue_s(n, b0 + 1 == b1);
-        for (int b = b0; ok && b < b1; ++b, ++n) {
-          if (b + 1 < b1) issue_s(n + 1, b + 2 == b1);
-          if (ok && b == b0 && sg > 0) ok = warp_wait<true>(&bars->o_free, (sg - 1) & 1, wc);
-          if (ok) issue_o(n, b == b0);
-        }
-        ++sg;
       }
       if (elect_one()) pair_commit(&bars->drain);
       mbar_wait(&bars->drain, 0, drain_ctx);
