@@ -286,9 +286,6 @@ struct SegIter {
     at.block = 0;
     return true;
   }
-  // The same as a call, for the warp that issues the products: with the search inlined there the
-  // compiler's code for the loop of products is slower (1024 tokens over 16384: 4.1 ms, not 3.7).
-  __device__ __noinline__ bool next_call(Segment& g) { return next(g); }
 };
 
 // The merge's record of a part, by one thread.

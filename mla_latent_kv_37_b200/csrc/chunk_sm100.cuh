@@ -27,8 +27,8 @@
 //
 // Bound by the tensor pipe, 2176 flops per visible pair of row and key, and behind it by the power
 // limit: 1024 tokens over 16384 rows, 128 heads 3.3 ... 3.7 ms, 1.23 ... 1.37 PFLOP/s (a library
-// matrix product runs at 1.37 for seconds on end).  32 x 4 tokens over 4096 ... 8126 rows: 187 ...
-// 225 us.  Eight single tokens: 26 us, of which the first copies' latency, the partial results and
+// matrix product runs at 1.37 for seconds on end).  32 x 4 tokens over 4096 ... 8126 rows: 185 ...
+// 225 us.  Eight single tokens: 24 us, of which the first copies' latency, the partial results and
 // their merge are the most.
 #pragma once
 #include "chunk_plan.cuh"
@@ -50,7 +50,7 @@ constexpr uint32_t kOffK = kOffQ + 9 * kBoxBytes;
 constexpr uint32_t kOffV = kOffK + kKUnits * kKUnit;
 constexpr uint32_t kOffP = kOffV + kVUnits * kVUnit;
 constexpr uint32_t kOffBar = kOffP + 2 * kBoxBytes;
-constexpr uint32_t kSmemBytes = kOffBar + 1536 + 1024;
+constexpr uint32_t kSmemBytes = kOffBar + 1536;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -100,9 +100,8 @@ __device__ __forceinline__ void pair_barrier(int id) {  // 64 threads: warps w a
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
                 const __grid_constant__ Params p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (1024-byte atoms of the swizzle; a base known when compiling makes constants of the descriptors)
+  extern __shared__ __align__(1024) uint8_t smem[];
   ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem + kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();

@@ -7,10 +7,13 @@
 // for 128 keys where a CTA of its own moves 80 KB, and its tensor core reads 6 KB instead of 8 KB of
 // shared memory for a 128 x 128 x 16 product.  At full load the GPU runs at its power limit, so that
 // this is what the rate depends on.
-// One prompt of 16384 tokens, 32 query and 4 key heads: 2.30 ... 2.46 ms, 1.12 ... 1.2 PFLOP/s, where
-// CTAs of their own take 2.50 ... 2.62 ms.
-// Softmax, order of the products and tensor memory are those of prompt_sm100.cuh; the leader (CTA 0)
-// issues for both, so barriers that it waits on collect both CTAs' arrivals.
+// One prompt of 16384 tokens, 32 query and 4 key heads: 2.23 ... 2.44 ms, 1.13 ... 1.23 PFLOP/s, where
+// CTAs of their own take 2.50 ... 2.66 ms.
+// Softmax and tensor memory are those of prompt_sm100.cuh; the leader (CTA 0) issues for both, so
+// barriers that it waits on collect both CTAs' arrivals.  A tile's products are issued by a warp of
+// its own, in the order PV(j) S(j+1): neither tile's waits hold up the other (2.32 ms with one
+// warp).  Three stages of keys and values let the tiles drift apart; the single CTA's ring does not
+// (8192 tokens in six prompts: 1.05 ms with one issuer, 1.15 ms with two), so it has one.
 #pragma once
 #include "packed.cuh"
 #include "prompt_sm100.cuh"
@@ -21,7 +24,7 @@ namespace prompt_pair {
 
 using prompt::kTile;
 constexpr int kRows = 4 * kTile;    // query rows of a pair
-constexpr int kThreads = 320;       // 8 softmax warps (4 a tile), TMA producer, MMA issuer
+constexpr int kThreads = 352;       // 8 softmax warps (4 a tile), TMA producer, an MMA issuer a tile
 constexpr uint32_t kBox = kTile * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kKStage = 3 * kBox / 2, kVStage = kBox;
 constexpr int kStages = 3;
@@ -29,7 +32,7 @@ constexpr uint32_t kOffQ = 0;                            // [2 tiles][3 boxes]
 constexpr uint32_t kOffK = kOffQ + 6 * kBox;             // [kStages][3 boxes of 64 keys]
 constexpr uint32_t kOffV = kOffK + kStages * kKStage;    // [kStages][128 keys x 64 columns]
 constexpr uint32_t kOffBar = kOffV + kStages * kVStage;
-constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
+constexpr uint32_t kSmemBytes = kOffBar + 512;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 using prompt::kDrainNs;
 using prompt::kRescaleThreshold;
@@ -41,17 +44,17 @@ using prompt::kTmemS;
 struct Bars {
   uint64_t q_full[2];         // L: a tile's queries landed (bytes of both CTAs)
   uint64_t k_full[kStages];   // L: a key tile landed (bytes of both CTAs)
-  uint64_t k_empty[kStages];  // both tiles' S have read it (commit)
+  uint64_t k_empty[kStages];  // a tile's S has read it (commit, one a tile)
   uint64_t v_full[kStages];   // L: both CTAs' halves of a value tile landed (2, and bytes)
-  uint64_t v_empty[kStages];  // both tiles' PV have read it (commit)
+  uint64_t v_empty[kStages];  // a tile's PV has read it (commit, one a tile)
   uint64_t v_tail;            // the sequence's last value tile landed, where it has to be cleared
   uint64_t s_full[2];         // a tile's S is written (commit)
   uint64_t p_half[2];         // L: the tile's softmax warps: P of 64 keys written, O rescaled (8)
   uint64_t p_full[2];         // L: the same: all of P written (8)
   uint64_t o_full[2];         // the tile's last PV is done (commit)
-  uint64_t drain;
+  uint64_t drain[2];          // an issuer's products are done (commit)
   uint32_t tmem_base;
-  int steps[2], len;          // key tiles of the two query tiles, tokens: for the MMA issuer
+  int steps[2], len;          // key tiles of the two query tiles, tokens: for the MMA issuers
   int abort_flag;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
@@ -60,9 +63,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_v,
                 const prompt::Params p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -93,12 +94,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_empty[i], 2);
       mbar_init(&bars->v_full[i], 2);
-      mbar_init(&bars->v_empty[i], 1);
+      mbar_init(&bars->v_empty[i], 2);
     }
     mbar_init(&bars->v_tail, 1);
-    mbar_init(&bars->drain, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->drain[i], 1);
     bars->abort_flag = 0;
     bars->steps[0] = n0;
     bars->steps[1] = n1;
@@ -172,80 +173,74 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
         mbar_wait(&bars->k_empty[i % kStages], (i / kStages) & 1, wc);
         mbar_wait(&bars->v_empty[i % kStages], (i / kStages) & 1, wc);
       }
-  } else if (warp == 9) {
-    // =================== MMA issuer (the leader's) ===================
+  } else if (warp >= 9) {
+    // =================== MMA issuers (the leader's), one a tile ===================
     // (the counts are read back from shared memory: see prompt_sm100.cuh)
     if (rank == 0) {
+      const int t = warp - 9;
       const volatile Bars* vb = bars;
-      const int n0 = vb->steps[0], n1 = vb->steps[1], len = vb->len, n_max = max(n0, n1);
+      const int n = vb->steps[t], len = vb->len, n_max = max(n, vb->steps[t ^ 1]);
       const uint32_t id = idesc_bf16(2 * kTile, kTile, 0, 0), id_o = idesc_bf16(2 * kTile, 128, 0, 1);
-      const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
+      const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ + 3 * t * kBox), 16, 1024, kSwizzle128B);
       const uint64_t d_k = smem_desc(smem_u32(smem + kOffK), 16, 1024, kSwizzle128B);
       const uint64_t d_v = smem_desc(smem_u32(smem + kOffV), kBox, 1024, kSwizzle128B);
+      const uint32_t tS = tmem + kTmemS + kTile * t, tO = tmem + kTmemO + 128 * t;
       const auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
-      bool ok = true;
-      // the first tile to use a key or value tile waits for it, the last one releases it
-      const auto issue_s = [&](int t, int j) {
-        const bool first = t == 0 || j >= n0, last = t == 1 || j >= n1;
-        const int s = j % kStages;
-        if (j == 0) ok = ok && warp_wait(&bars->q_full[t], 0, wc);
-        if (first) ok = ok && warp_wait(&bars->k_full[s], (j / kStages) & 1, wc);
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
+      bool ok = n == 0 || warp_wait(&bars->q_full[t], 0, wc);
+      for (int j = -1; ok && j < n; ++j) {
+        if (j >= 0) {  // O += P V
+          const int s = j % kStages, steps = (min(kTile, len - j * kTile) + 15) / 16;
+          const uint64_t b = at(d_v, s * kVStage);
+          ok = warp_wait(&bars->v_full[s], (j / kStages) & 1, wc);
 #pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint64_t a = at(d_q, (3 * t + c) * kBox);
-            const uint64_t b = at(d_k, s * kKStage + c * (kBox / 2));
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && warp_wait(half ? &bars->p_full[t] : &bars->p_half[t], j & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              if (steps == kTile / 16) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pair_mma_ss(tmem + kTmemS + kTile * t, at(a, 32 * k), at(b, 32 * k), id, c > 0 || k > 0);
+                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                  pair_mma_ts(tO, tS + 8 * k, at(b, 2048 * k), id_o, k > 0 || j > 0);
+              } else {
+                for (int k = 4 * half; k < min(4 * half + 4, steps); ++k)
+                  pair_mma_ts(tO, tS + 8 * k, at(b, 2048 * k), id_o, k > 0 || j > 0);
+              }
+              if (half) pair_commit(&bars->v_empty[s]);
+              if (half && j == n - 1) pair_commit(&bars->o_full[t]);
+            }
           }
-          if (last) pair_commit(&bars->k_empty[s]);
-          pair_commit(&bars->s_full[t]);
         }
-      };
-      const auto issue_pv = [&](int t, int j) {
-        const bool first = t == 0 || j >= n0, last = t == 1 || j >= n1;
-        const int s = j % kStages;
-        if (first) ok = ok && warp_wait(&bars->v_full[s], (j / kStages) & 1, wc);
-        const int steps = (min(kTile, len - j * kTile) + 15) / 16;
-        const uint64_t b = at(d_v, s * kVStage);
-        const uint32_t o = tmem + kTmemO + 128 * t, a = tmem + kTmemS + kTile * t;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && warp_wait(half ? &bars->p_full[t] : &bars->p_half[t], j & 1, wc);
-          if (!ok) return;
+        if (j + 1 < n) {  // the next S, over P
+          const int s = (j + 1) % kStages;
+          if (!(ok = ok && warp_wait(&bars->k_full[s], ((j + 1) / kStages) & 1, wc))) break;
           tc_fence_after();
           if (elect_one()) {
-            if (steps == kTile / 16) {
 #pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                pair_mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, k > 0 || j > 0);
-            } else {
-              for (int k = 4 * half; k < min(4 * half + 4, steps); ++k)
-                pair_mma_ts(o, a + 8 * k, at(b, 2048 * k), id_o, k > 0 || j > 0);
+            for (int c = 0; c < 3; ++c) {
+              const uint64_t a = at(d_q, c * kBox), b = at(d_k, s * kKStage + c * (kBox / 2));
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                pair_mma_ss(tS, at(a, 32 * k), at(b, 32 * k), id, c > 0 || k > 0);
             }
-            if (half && last) pair_commit(&bars->v_empty[s]);
-            if (half && j == (t ? n1 : n0) - 1) pair_commit(&bars->o_full[t]);
+            pair_commit(&bars->k_empty[s]);
+            pair_commit(&bars->s_full[t]);
           }
         }
-      };
-      issue_s(0, 0);
-      if (n1 > 0) issue_s(1, 0);
-      for (int j = 0; ok && j < n_max; ++j) {
-        if (j < n0) {
-          issue_pv(0, j);
-          if (ok && j + 1 < n0) issue_s(0, j + 1);
-        }
-        if (ok && j < n1) {
-          issue_pv(1, j);
-          if (ok && j + 1 < n1) issue_s(1, j + 1);
+      }
+      // the steps of the other tile alone
+      for (int j = n; ok && j < n_max; ++j) {
+        if (j >= kStages)  // (not before this tile's share of the slot's last release)
+          ok = warp_wait(&bars->k_empty[j % kStages], (j / kStages - 1) & 1, wc) &&
+               warp_wait(&bars->v_empty[j % kStages], (j / kStages - 1) & 1, wc);
+        if (ok && elect_one()) {
+          pair_commit(&bars->k_empty[j % kStages]);
+          pair_commit(&bars->v_empty[j % kStages]);
         }
       }
       // no MMA may be in flight when TMEM is released
-      if (elect_one()) pair_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0, drain_ctx);
+      if (elect_one()) pair_commit(&bars->drain[t]);
+      mbar_wait(&bars->drain[t], 0, drain_ctx);
     }
   } else {
     // =================== softmax: warps 4t ... 4t + 3 own tile t, a thread one row ==========
@@ -354,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9 && lane == 0 && rank == 1) mbar_wait(&bars->drain, 0, drain_ctx);
+  if (warp >= 9 && lane == 0 && rank == 1) mbar_wait(&bars->drain[warp - 9], 0, drain_ctx);
   __syncwarp();
   cluster_sync();
   uint32_t peer_abort;

@@ -46,7 +46,7 @@ constexpr uint32_t kOffQ = 0;                        // [2 tiles][3 boxes]
 constexpr uint32_t kOffK = kOffQ + 6 * kBox;         // [kKSlots]
 constexpr uint32_t kOffV = kOffK + kKSlots * kBox;   // [kVSlots][2 boxes]
 constexpr uint32_t kOffBar = kOffV + kVSlots * 2 * kBox;
-constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
+constexpr uint32_t kSmemBytes = kOffBar + 512;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -84,9 +84,7 @@ __global__ void __maxnreg__(168)
     prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_v,
                   const Params p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();

@@ -332,7 +332,7 @@ def test_prompt_long():
     c.check(o, l, heads=[0, 15])
 
 
-@pytest.mark.parametrize("tokens,H,Hk", [([4096], 16, 16), ([8000, 37, 4300], 16, 2), ([4737, 0, 7655], 32, 4)],
+@pytest.mark.parametrize("tokens,H,Hk", [([4096], 16, 16), ([2100, 2000], 16, 1), ([8000, 37, 4300], 16, 2), ([4737, 0, 7655], 32, 4)],
                          ids=lambda v: str(v))
 def test_prompt_pairs(tokens, H, Hk):
     # long on average: two SMs share every product; sequences that end inside a tile, a short one and
