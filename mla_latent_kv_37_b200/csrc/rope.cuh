@@ -26,10 +26,12 @@ __device__ __forceinline__ float2 rope_cs(float theta, int pair, int pos) {
   return rope_cs(pow(static_cast<double>(theta), -2.0 * pair / 64.0), pos);
 }
 
-// theta^(-2 pair / 64) of the 32 pairs, for kernels that take them as parameters.
+// theta^(-2 pair / 64) of the 32 pairs, for kernels that take them as parameters: 2^x, whose relative
+// error is that of x times |x| ln 2, largest against the angle where 2^x |x| is: 1.6e-7 rad at
+// position 2^31.
 inline void rope_frequencies(float theta, double (&inv_freq)[32]) {
-  for (int pair = 0; pair < 32; ++pair)
-    inv_freq[pair] = std::pow(static_cast<double>(theta), -2.0 * pair / 64.0);
+  const double step = std::log2(static_cast<double>(theta)) / 32;
+  for (int pair = 0; pair < 32; ++pair) inv_freq[pair] = std::exp2(-step * pair);
 }
 
 }  // namespace mla
