@@ -1,5 +1,5 @@
 // Attention of several query rows on the SIMT cores with fp32 products (the fp32 configuration:
-// the tensor cores have no mode accurate to 1e-5), for whole packed prompts (192-wide keys,
+// no product of the tensor cores is exact to 1e-5), for whole packed prompts (192-wide keys,
 // 128-wide values) and for a chunk of new tokens over the paged latent cache (576 and 512).
 //
 // A block of W x KS warps takes 8 W query rows and walks over the keys 64 at a time with an online
@@ -16,7 +16,8 @@
 // the loads from shared memory: one of 16 bytes takes about four clocks of the SM, whether or not
 // the lanes read the same address, so 64 FMAs (16 clocks of the SM) that follow 8 loads (4 rows x
 // 4 keys a thread) take 32.  (2 x 8 and 8 x 2 follow 10; a slice of 64 rows x 64 keys measured
-// 4450 clocks with them.)
+// 4450 clocks with them.)  Prompts of 500, 129 and 33 tokens, 16 heads: 97 us (14 TFLOP/s); 33 and 7
+// tokens over 700 and 129 rows: 47 us and the merge.
 #pragma once
 #include "chunk_plan.cuh"
 

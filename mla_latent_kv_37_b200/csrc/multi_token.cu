@@ -156,9 +156,9 @@ int mla_append_rows(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_to
   const unsigned blocks = (static_cast<unsigned>(n_tokens) + rows::kTokens - 1) / rows::kTokens;
   const bool bf16 = dims->dtype == MLA_BF16;
   const int heads = bf16 ? rows::Chunk<__nv_bfloat16>::kHeads : rows::Chunk<float>::kHeads;
-  const unsigned slices = q_rope ? (dims->n_heads + heads - 1) / heads : 0;
+  p.slices = 1 + (q_rope ? (dims->n_heads + heads - 1) / heads : 0);
   host_launch(bf16 ? rows::append_rows_kernel<__nv_bfloat16> : rows::append_rows_kernel<float>,
-              dim3(blocks, 1 + slices), dim3(rows::kThreads), 0,
+              dim3(blocks * p.slices), dim3(rows::kThreads), 0,
               reinterpret_cast<cudaStream_t>(stream), p);
   return host_launched();
 }
