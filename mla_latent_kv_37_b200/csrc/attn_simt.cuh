@@ -433,7 +433,7 @@ using ChunkLayout = Layout<576, 512, kChunkWarps, 1>;
 static_assert(ChunkLayout::kRows == 1 << kChunkTileShift, "a tile's rows");
 // Costs in quarters of a block of 16 keys: a segment's start and write-back take the time of about
 // two blocks (40 tokens of 16 heads over 829 rows: 61 us; 79 us with half a block for them).
-constexpr int kChunkBlockCost = 4, kChunkSegCost = 8, kChunkLeast = 4;
+constexpr int kChunkCostShift = 2, kChunkSegCost = 8, kChunkLeast = 4;
 
 __global__ void __launch_bounds__(ChunkLayout::kThreads, 1) chunk_kernel(const ChunkParams p) {
   extern __shared__ __align__(16) float smem[];

@@ -32,7 +32,8 @@ constexpr int kPage = 64, kRow = 576, kDc = 512;
 struct Shape {
   int n_tokens, batch, n_heads, max_pages;
   int tile_shift, block_shift;  // 2^ rows of a tile, keys of a block
-  int block_cost, seg_cost, least;  // least: no part is worth less (but for a lone one)
+  int cost_shift, seg_cost, least;  // 2^ cost of a block; cost of a segment's start and end; no
+                                    // part is worth less than `least` (but for a lone one)
   const int32_t* cu;
   const int32_t* seq_lens;
 };
@@ -125,41 +126,49 @@ constexpr int kMaxSplit = 24;
 // Caches of fewer rows stay in L2 (37 MB of 126) whatever the order.
 constexpr int64_t kTeamKeys = 32768;
 
-// The parts of a team (1: no teams).  All threads of the block.
-__device__ inline int team_size(const Shape& s, int parts, int64_t* warp_sums) {
-  const int w = tiles_of(s, packed::span(s.cu, 0, s.n_tokens).size());
-  if (w < 2 || parts / w * w * 16 < parts * 15) return 1;
-  int64_t keys = 0, total;
-  for (int b0 = 0; b0 < s.batch; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    const bool in = b < s.batch;
-    if (!__syncthreads_and(!in || tiles_of(s, packed::span(s.cu, b, s.n_tokens).size()) == w)) return 1;
-    if (in) keys += clamped_len(s, b);
-  }
-  block_scan(keys, warp_sums, &total);
-  return total >= kTeamKeys ? w : 1;
-}
-
 // The range of part `part` of `parts`.  All threads of the block.
 __device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* sc,
                                   unsigned int* status) {
   const int T = blockDim.x, tid = threadIdx.x;
   bool bad = false;
-  const int w = team_size(s, parts, sc->warp_sums), rank = part / w, ranks = parts / w;
+  // this thread's sequence of a round, to the scratch
+  const auto load_round = [&](int b0) {
+    const int b = b0 + tid;
+    int size = 0;
+    if (b < s.batch) {
+      const int len = s.seq_lens[b];
+      size = packed::span(s.cu, b, s.n_tokens, &bad).size();
+      sc->len[tid] = min(max(len, 0), s.max_pages * kPage);
+      bad |= len < 0 || len > s.max_pages * kPage;
+    }
+    sc->size[tid] = size;
+    __syncthreads();
+  };
+  load_round(0);
+  // the parts of a team: as many as each sequence has tiles, or 1
+  int w = tiles_of(s, sc->size[0]);
+  if (w < 2 || parts / w * w * 16 < parts * 15) w = 1;
+  if (w > 1) {
+    int64_t keys = 0, total;
+    for (int b0 = 0; w > 1 && b0 < s.batch; b0 += T) {
+      if (b0 > 0) load_round(b0);
+      const bool in = b0 + tid < s.batch;
+      if (in) keys += sc->len[tid];
+      if (!__syncthreads_and(!in || tiles_of(s, sc->size[tid]) == w)) w = 1;
+    }
+    block_scan(keys, sc->warp_sums, &total);
+    if (total < kTeamKeys) w = 1;
+  }
+  const int rank = part / w, ranks = parts / w;
   // f(place of an entry, its cost or 0 without one), a round of T entries at a time; their number
   const auto each_round = [&](auto&& f) {
     int base = 0;
     for (int b0 = 0; b0 < s.batch; b0 += T) {
-      const int b = b0 + tid;
-      int size = 0, n = 0;
-      if (b < s.batch) {
-        const int len = s.seq_lens[b];
-        size = packed::span(s.cu, b, s.n_tokens, &bad).size();
-        n = w > 1 ? 1 : tiles_of(s, size);
-        sc->len[tid] = min(max(len, 0), s.max_pages * kPage);
-        bad |= len < 0 || len > s.max_pages * kPage;
+      if (s.batch > T) {
+        __syncthreads();
+        load_round(b0);
       }
-      sc->size[tid] = size;
+      const int n = b0 + tid < s.batch ? (w > 1 ? 1 : tiles_of(s, sc->size[tid])) : 0;
       int64_t total;
       sc->first[tid] = static_cast<int>(block_scan(n, sc->warp_sums, &total));
       __syncthreads();
@@ -181,7 +190,7 @@ __device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* 
           t.rows = min(1 << s.tile_shift, sc->size[lo] * s.n_heads - t.row0);
           t.len = sc->len[lo];
           t.first = t.len - sc->size[lo];
-          cost = s.seg_cost + static_cast<int64_t>(s.block_cost) * t.blocks(s);
+          cost = s.seg_cost + (static_cast<int64_t>(t.blocks(s)) << s.cost_shift);
         }
         f(at, cost);
       }
@@ -202,7 +211,7 @@ __device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* 
     ++rounds;
   });
   if (bad && part == 0) atomicOr(status, MLA_STATUS_BAD_LENGTH);
-  // part c begins at place floor(c V / C).  least >= block_cost, so no two begin at the same block
+  // part c begins at place floor(c V / C).  `least` is a block's cost or more, so no two begin at the same block
   // past a tile's first.
   const int most = min(static_cast<int64_t>(ranks), kMaxSplit * static_cast<int64_t>(entries));
   const int C = V >= static_cast<int64_t>(most) * s.least
@@ -222,7 +231,7 @@ __device__ inline Range find_part(const Shape& s, int parts, int part, Scratch* 
       if (v0 <= u[e] && u[e] < v0 + cost) {
         sc->found[e] = at;
         if (u[e] - v0 > s.seg_cost)
-          sc->found[e].block = static_cast<int>((u[e] - v0 - s.seg_cost) / s.block_cost);
+          sc->found[e].block = static_cast<int>((u[e] - v0 - s.seg_cost) >> s.cost_shift);
       }
   };
   if (tid == 0) sc->found[1] = Place{s.batch, 0, 0, 0x7fffffff};  // behind the last tile

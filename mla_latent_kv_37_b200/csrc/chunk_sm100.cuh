@@ -40,7 +40,7 @@ constexpr int kTileShift = 7, kTileRows = 1 << kTileShift, kCtaRows = 64;
 constexpr int kBlockShift = 7, kBlock = 1 << kBlockShift;  // keys per block: two pages
 // Costs in blocks: a segment's start and write-back take the time of about four.  Parts of at least
 // four: eight single tokens over 64 ... 3000 keys take 25 us, 27 us with parts of two.
-constexpr int kBlockCost = 1, kSegCost = 4, kLeast = 4;
+constexpr int kCostShift = 0, kSegCost = 4, kLeast = 4;
 constexpr int kThreads = 256;  // 4 softmax warps, key producer, S issuer, value producer, O issuer
 constexpr uint32_t kBoxBytes = 64 * 128;  // 64 rows x 64 bf16
 constexpr int kKUnits = 3, kVUnits = 4;

@@ -291,7 +291,7 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
   const chunk::Shape shape{n_tokens, dims->batch, dims->n_heads, max_pages,
                            bf16 ? chunk::kTileShift : simt::kChunkTileShift,
                            bf16 ? chunk::kBlockShift : simt::kChunkBlockShift,
-                           bf16 ? chunk::kBlockCost : simt::kChunkBlockCost,
+                           bf16 ? chunk::kCostShift : simt::kChunkCostShift,
                            bf16 ? chunk::kSegCost : simt::kChunkSegCost,
                            bf16 ? chunk::kLeast : simt::kChunkLeast, cu_tokens, seq_lens};
   chunk::PartStart* starts = reinterpret_cast<chunk::PartStart*>(ws + w.starts);
