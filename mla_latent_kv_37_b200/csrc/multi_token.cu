@@ -26,8 +26,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t elem_size(const mla_dims* d) { return d->dtype == MLA_BF16 ? 2 : 4; }
-// A stride (elements) of 16-byte multiples that does not run backwards; `least` elements lie
-// between two neighbours.  Zero is the one exception: all of them are the same.
+// A stride (elements) of 16-byte multiples under which neighbours of `least` elements do not overlap;
+// strides of zero or backwards are refused.
 bool stride_ok(int64_t stride, int64_t least, size_t elem) {
   return stride >= least && stride < (int64_t{1} << 36) && stride * static_cast<int64_t>(elem) % 16 == 0;
 }

@@ -22,7 +22,7 @@
 // set to zero first, since a weight of zero does not silence a NaN.
 //
 // Bound by the tensor pipe, 640 flops per visible pair of rows and head, and behind it by the power
-// limit (1 kW, 1.7 GHz instead of 1.9).  8192 tokens in six prompts, 128 heads: 1.06 ... 1.13 ms,
+// limit (1 kW, 1.7 GHz instead of 1.9).  8192 tokens in six prompts, 128 heads: 1.06 ... 1.18 ms,
 // 0.82 ... 0.87 PFLOP/s.  Two tiles fill 53% of the pipe's clocks: a tile's softmax (2100 clocks) and
 // its products (1280) follow one another, since P lies over S.  What was tried against that: P in
 // shared memory, so that S(j+1) need not wait for PV(j) (3.4 ms instead of 2.6 ms for one prompt of
