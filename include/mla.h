@@ -31,7 +31,9 @@
  *     MLA_STATUS_TIMEOUT; the kernel then waits (on its own, longer limit) for the copies and
  *     tensor-core operations it has in flight, releases its resources and returns, and the
  *     CUDA context stays usable.  MLA_TEST_STALL=1 (read at each call) makes one warp of the
- *     decode kernel wait on a barrier nothing arrives on, to exercise that path in tests.
+ *     decode kernel wait on a barrier nothing arrives on, to exercise that path in tests; for the
+ *     bf16 attention of several new tokens, MLA_TEST_STALL=n stalls warp n - 1 of every CTA
+ *     (n < 100), or, with 100 or 200 added, of the first or second CTA of each pair alone.
  *   - Weights are row-major [out_features, in_features] (column-vector form, [TN]):
  *       w_dkv [d_c, D], w_kr [d_rope, D], w_q [H*(d_nope+d_rope), D] (per head d_nope rows then
  *       d_rope rows), w_uk [H*d_nope, d_c], w_uv [H*d_v, d_c], w_o [D, H*d_v].

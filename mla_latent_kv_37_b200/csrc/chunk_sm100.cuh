@@ -69,16 +69,18 @@ struct Params {
   float* part_lse;
   unsigned int* status;
   uint64_t wait_ns;
+  int stall;  // see host_stall
 };
 
+constexpr int kLoadBars = 1 + kKUnits + kVUnits;  // the first barriers: of copies
 // Barriers marked L are the leader's (CTA 0): the MMA issuer waits there for both CTAs.  The
 // others are each CTA's own; a commit arrives at both CTAs'.
 struct ChunkBars {
   uint64_t q_full;            // L: the segment's queries landed (bytes of both CTAs)
-  uint64_t q_empty;           // the segment's last S is done (commit)
   uint64_t k_full[kKUnits];   // L: a key unit landed (bytes of both CTAs)
-  uint64_t k_empty[kKUnits];  // S has read the unit (commit)
   uint64_t v_full[kVUnits];   // L: both CTAs' value units landed (2, and bytes)
+  uint64_t q_empty;           // the segment's last S is done (commit)
+  uint64_t k_empty[kKUnits];  // S has read the unit (commit)
   uint64_t v_empty[kVUnits];  // O has read the unit (commit)
   uint64_t s_full[2];         // S of a block is written (commit)
   uint64_t s_free[2];         // L: the softmax warps of both CTAs have read S (8)
@@ -87,14 +89,34 @@ struct ChunkBars {
   uint64_t o_free;            // L: the softmax warps of both CTAs have drained O (8)
   uint64_t v_tail[kVUnits];   // a value unit with rows past the sequence's end landed (bytes)
   uint64_t drain;             // both issuers' products are done (2 commits)
+  uint64_t stall;             // nothing ever arrives here (test of a wait that runs out)
   uint32_t tmem_base;
   int abort_flag;
+  // what the producers (warps 4 and 6) have issued: blocks begun, segments or ragged blocks begun, and
+  // where a wait that ran out left the last of them (0: nowhere)
+  int blocks[8], rest[8], left[8];
+  int loads[kLoadBars];       // from that, phases of q_full, k_full[], v_full[]
   float xch[2][kTileRows];    // the two halves of a row exchange maxima (block parity) and sums
 };
 static_assert(sizeof(ChunkBars) <= 1536, "barrier block");
 
 __device__ __forceinline__ void pair_barrier(int id) {  // 64 threads: warps w and w ^ 2
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+// After an abort, by a producer's warp: the phases of its barriers that it has had its part in; and its
+// copies that no v_full counts yet, those of a ragged block, have landed.
+enum { kLeftQ = 1, kLeftUnit = 16, kLeftRagged = 32, kLeftTail = 48 };
+__device__ __forceinline__ void issued_loads(ChunkBars* bars, int warp, int lane, const WaitCtx& w) {
+  const bool keys = warp == 4;
+  const int units = keys ? kKUnits : kVUnits, n = bars->blocks[warp], rest = bars->rest[warp];
+  const int left = bars->left[warp], at = left & ~15, u = left & 15;
+  // units issued (of values, announced): all, or up to unit u of the last block
+  const int issued = at == 0 ? units * n : units * (n - 1) + (at == kLeftRagged ? 0 : u);
+  if (lane < units) bars->loads[(keys ? 1 : 1 + kKUnits) + lane] = (issued + units - 1 - lane) / units;
+  if (keys && lane == 0) bars->loads[0] = left == kLeftQ ? rest - 1 : rest;
+  if (lane < (at == kLeftTail ? kVUnits : at == kLeftRagged ? u : 0))
+    mbar_wait(&bars->v_tail[lane], (rest - 1) & 1, w);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -130,7 +152,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->o_free, 8);
     mbar_init(&bars->drain, 2);
+    mbar_init(&bars->stall, 1);
     bars->abort_flag = 0;
+    bars->left[4] = bars->left[6] = 0;
     fence_mbar_init_cluster();
   }
   if (warp == 5) {
@@ -151,6 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       find_part(p.shape, p.parts, part, reinterpret_cast<Scratch*>(smem + kOffP), p.status);
   if (rank == 0 && threadIdx.x == 0) write_start(p.shape, range, p.starts + part);
   __syncthreads();  // P's place held the scratch
+  if (p.stall != 0 && stall_here(p.stall, warp, rank)) (void)warp_wait(&bars->stall, 0, wc);
   SegIter it(p.shape, range);
   Segment seg;
 
@@ -159,6 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool keys = warp == 4;
     bool ok = true;
     int n = 0, sg = 0, tails = 0;  // blocks, non-empty segments, and ragged blocks so far
+    int* note = &bars->left[warp];
     while (ok && it.next(seg)) {
       const Tile t = seg.t;
       const int b0 = seg.b0, b1 = seg.b1;
@@ -166,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int32_t* table = p.page_table + static_cast<int64_t>(t.seq) * p.shape.max_pages;
       const int pages = (t.visible(t.rows - 1, H) + kPage - 1) / kPage;
       if (keys) {
-        if (sg > 0) ok = warp_wait(&bars->q_empty, (sg - 1) & 1, wc);
+        if (sg > 0) ok = warp_wait_noted(&bars->q_empty, (sg - 1) & 1, wc, note, kLeftQ);
         if (ok && elect_one()) {
           const uint32_t bar = mapa_shared(smem_u32(&bars->q_full), 0);
           if (rank == 0) mbar_arrive_expect_tx(&bars->q_full, 2 * 9 * kBoxBytes);
@@ -194,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int y = rank ? y1 : y0;
 #pragma unroll
             for (int u = 0; u < kKUnits; ++u) {
-              if (ok && n > 0) ok = warp_wait(&bars->k_empty[u], (n - 1) & 1, wc);
+              if (ok && n > 0) ok = warp_wait_noted(&bars->k_empty[u], (n - 1) & 1, wc, note, kLeftUnit + u);
               if (ok && elect_one()) {
                 if (rank == 0) mbar_arrive_expect_tx(&bars->k_full[u], 2 * kKUnit);
                 const uint32_t bar = mapa_shared(smem_u32(&bars->k_full[u]), 0);
@@ -208,7 +234,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int u = 0; u < kVUnits; ++u) {
-            if (ok && n > 0) ok = warp_wait(&bars->v_empty[u], (n - 1) & 1, wc);
+            if (ok && n > 0)
+              ok = warp_wait_noted(&bars->v_empty[u], (n - 1) & 1, wc, note,
+                                   (ragged ? kLeftRagged : kLeftUnit) + u);
             if (ok && elect_one()) {
               const uint32_t bar = ragged ? smem_u32(&bars->v_tail[u])
                                           : mapa_shared(smem_u32(&bars->v_full[u]), 0);
@@ -224,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // what the pool holds past the sequence's end must not reach the product: a weight of
           // zero does not silence a NaN
           for (int u = 0; ok && u < kVUnits; ++u) {
-            if (!(ok = warp_wait(&bars->v_tail[u], tails & 1, wc))) break;
+            if (!(ok = warp_wait_noted(&bars->v_tail[u], tails & 1, wc, note, kLeftTail + u))) break;
             for (int i = lane; i < 2 * 64 * 8; i += 32) {
               const int key = (i >> 3) & 63;
               if (64 * (u >> 1) + key >= held)
@@ -239,6 +267,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       ++sg;
+    }
+    if (lane == 0) {
+      bars->blocks[warp] = n;
+      bars->rest[warp] = keys ? sg : tails;
     }
     // the last releases arrive at both CTAs' barriers; a CTA does not exit before it has seen them
     if (ok && n > 0 && lane == 0) {
@@ -490,15 +522,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 5 && lane == 0 && rank == 1) mbar_wait(&bars->drain, 0, drain_ctx);
   __syncwarp();
   cluster_sync();
-  uint32_t peer_abort;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];"
-               : "=r"(peer_abort)
-               : "r"(mapa_shared(smem_u32(&bars->abort_flag), rank ^ 1u)));
-  // after an abort, copies and remote arrivals that nobody waited for may still be on their way
-  if (bars->abort_flag != 0 || peer_abort != 0) {
+  // After an abort the leader waits for the copies of both CTAs, whose shared memory nothing may
+  // write any more when they exit (a unit's phase is issued only when its last one has been used, so
+  // that the last of all is the only one that can be open).  Remote arrivals that nobody waited for may
+  // still be on their way too.
+  if (bars->abort_flag != 0 || pair_peer_word(&bars->abort_flag, rank) != 0) {
+    if (warp == 4 || warp == 6) issued_loads(bars, warp, lane, drain_ctx);
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();
+    if (rank == 0 && threadIdx.x < kLoadBars) {
+      const int b = threadIdx.x, mine = bars->loads[b], others = pair_peer_word(&bars->loads[b], 0);
+      pair_close(&bars->q_full + b, max(mine, others) - 1, mine >= others, others >= mine,
+                 b == 0 ? 9 * kBoxBytes : b <= kKUnits ? kKUnit : kVUnit, b > kKUnits, drain_ctx);
+    }
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 1000000) {
     }
+    __syncwarp();
   }
   cluster_sync();
   if (warp == 5) {

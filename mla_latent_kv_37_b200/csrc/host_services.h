@@ -24,6 +24,8 @@ int host_cuda_error(cudaError_t e, const char* where);
 int host_launched(int kernels = 1);
 bool host_pdl();
 uint64_t host_wait_ns();
+// MLA_TEST_STALL of the environment, read at each call: 0 unless it is a number from 1 to 299.
+int host_stall();
 // The checks of mla_dims that do not limit the batch.
 int host_check_dims(const mla_dims* d);
 int host_encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank,

@@ -48,6 +48,14 @@ int stall_test_requested() {
   const char* e = std::getenv("MLA_TEST_STALL");
   return (e && e[0] == '1' && e[1] == '\0') ? 1 : 0;
 }
+// The bf16 attention kernels of several new tokens stall a warp of the caller's choice: see stall_here.
+int stall_requested() {
+  const char* e = std::getenv("MLA_TEST_STALL");
+  if (!e || !*e) return 0;
+  char* end = nullptr;
+  const long v = std::strtol(e, &end, 10);
+  return *end == '\0' && v >= 1 && v <= 299 ? static_cast<int>(v) : 0;
+}
 constexpr int kMinPagesPerPart = 4;
 constexpr int kMaxParts = 1 << 16;  // upper bound on num_splits (host check before any arithmetic)
 constexpr int kSkMinUnits = 2;    // fewest stages' worth of weights a stream-K CTA streams
@@ -679,6 +687,7 @@ int host_cuda_error(cudaError_t e, const char* where) { return cuda_fail(e, wher
 int host_launched(int kernels) { return last_launch(kernels); }
 bool host_pdl() { return pdl_enabled(); }
 uint64_t host_wait_ns() { return wait_limit_ns(); }
+int host_stall() { return stall_requested(); }
 int host_check_dims(const mla_dims* d) { return check_dims(d, false); }
 int host_encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank,
                 const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,

@@ -216,7 +216,7 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
         (rc = map(&tv, v, kDv, n_kv_heads, v_head_stride, v_token_stride, prompt::kTile)))
       return rc;
     const prompt::Params p{n_tokens, dims->batch, dims->n_heads, n_kv_heads, cu_tokens, scale_log2,
-                           static_cast<__nv_bfloat16*>(o), lse, dev.status, host_wait_ns()};
+                           static_cast<__nv_bfloat16*>(o), lse, dev.status, host_wait_ns(), host_stall()};
     if (pair)
       host_launch(prompt_pair::pair_kernel, dim3(2 * tiles(prompt_pair::kRows), dims->n_heads),
                   dim3(prompt_pair::kThreads), prompt_pair::kSmemBytes, st, tq, tk, tkr, tv, p);
@@ -312,7 +312,8 @@ int mla_chunk_attn(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_tok
         (rc = map(&tc, cache_pool, static_cast<int64_t>(num_pages) * kPageN)))
       return rc;
     const chunk::Params p{shape, w.parts, num_pages, starts, page_table, scale_log2, o_lat,
-                          o_dtype == MLA_FP32, lse, part_o, part_lse, dev.status, host_wait_ns()};
+                          o_dtype == MLA_FP32, lse, part_o, part_lse, dev.status, host_wait_ns(),
+                          host_stall()};
     host_launch(chunk::pair_kernel, dim3(2 * w.parts), dim3(chunk::kThreads), chunk::kSmemBytes,
                 st, tq, tc, p);
   } else {

@@ -53,11 +53,15 @@ struct Bars {
   uint64_t p_full[2];         // L: the same: all of P written (8)
   uint64_t o_full[2];         // the tile's last PV is done (commit)
   uint64_t drain[2];          // an issuer's products are done (commit)
+  uint64_t stall;             // nothing ever arrives here (test of a wait that runs out)
   uint32_t tmem_base;
   int steps[2], len;          // key tiles of the two query tiles, tokens: for the MMA issuers
   int abort_flag;
+  int tiles_begun, left;      // of the producer, and where a wait that ran out left the last (0: nowhere)
+  int k_loads, v_loads;       // from that, its key tiles, and its value tiles announced on v_full
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
+enum { kLeftKeys = 1, kLeftValues, kLeftTail };
 
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -100,7 +104,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
     }
     mbar_init(&bars->v_tail, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bars->drain[i], 1);
+    mbar_init(&bars->stall, 1);
     bars->abort_flag = 0;
+    bars->left = 0;
     bars->steps[0] = n0;
     bars->steps[1] = n1;
     bars->len = len;
@@ -115,6 +121,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
   const WaitCtx wc{&bars->abort_flag, p.status, p.wait_ns};
   volatile int never = 0;
   const WaitCtx drain_ctx{&never, p.status, kDrainNs};
+  if (p.stall != 0 && stall_here(p.stall, warp, rank)) (void)warp_wait(&bars->stall, 0, wc);
 
   if (warp == 8) {
     // =================== TMA producer: this CTA's rows, keys and columns ===================
@@ -133,7 +140,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
     int j = 0;
     for (; j < n_max; ++j) {
       const int s = j % kStages, y = sp.begin + j * kTile;
-      if (j >= kStages) ok = warp_wait(&bars->k_empty[s], (j / kStages - 1) & 1, wc);
+      if (j >= kStages)
+        ok = warp_wait_noted(&bars->k_empty[s], (j / kStages - 1) & 1, wc, &bars->left, kLeftKeys);
       if (!ok) break;
       if (elect_one()) {
         const uint32_t bar = mapa_shared(smem_u32(&bars->k_full[s]), 0);
@@ -144,7 +152,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
                        c < 2 ? 64 * c : 0, c < 2 ? hk : 0, y + 64 * rank);
       }
       if (j == 0 && n1 > 0) load_q(1);
-      if (j >= kStages) ok = warp_wait(&bars->v_empty[s], (j / kStages - 1) & 1, wc);
+      if (j >= kStages)
+        ok = warp_wait_noted(&bars->v_empty[s], (j / kStages - 1) & 1, wc, &bars->left, kLeftValues);
       if (!ok) break;
       // values past the sequence's end, among the last 16 keys that PV reads, are cleared first: a
       // weight of zero does not silence a NaN
@@ -157,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
         pair_load_3d(smem + kOffV + s * kVStage, &tm_v, bar, 64 * rank, hk, y);
       }
       if (ragged) {
-        if (!(ok = warp_wait(&bars->v_tail, 0, wc))) break;
+        if (!(ok = warp_wait_noted(&bars->v_tail, 0, wc, &bars->left, kLeftTail))) break;
         const int end = (valid + 15) & ~15;
         for (int i = 8 * valid + lane; i < 8 * end; i += 32)
           *reinterpret_cast<uint4*>(smem + kOffV + s * kVStage + 16 * i) =
@@ -167,6 +176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
         if (lane == 0) arrive_cluster(mapa_shared(smem_u32(&bars->v_full[s]), 0));
       }
     }
+    if (lane == 0) bars->tiles_begun = j;
     // the last releases arrive at both CTAs' barriers; a CTA does not exit before it has seen them
     if (ok)
       for (int i = max(0, n_max - kStages); i < n_max; ++i) {
@@ -352,15 +362,34 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
   if (warp >= 9 && lane == 0 && rank == 1) mbar_wait(&bars->drain[warp - 9], 0, drain_ctx);
   __syncwarp();
   cluster_sync();
-  uint32_t peer_abort;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];"
-               : "=r"(peer_abort)
-               : "r"(mapa_shared(smem_u32(&bars->abort_flag), rank ^ 1)));
-  // after an abort, copies and remote arrivals that nobody waited for may still be on their way
-  if (bars->abort_flag != 0 || peer_abort != 0) {
+  // After an abort the leader waits for the copies of both CTAs, whose shared memory nothing may
+  // write any more when they exit (a stage's copies are issued only when its last ones have been used,
+  // so that only the last kStages of all can be open).  Remote arrivals that nobody waited for may still
+  // be on their way too.
+  if (bars->abort_flag != 0 || pair_peer_word(&bars->abort_flag, rank) != 0) {
+    if (threadIdx.x == 0) {
+      const int j = bars->tiles_begun, left = bars->left;
+      bars->k_loads = left == kLeftValues || left == kLeftTail ? j + 1 : j;
+      bars->v_loads = j;
+      if (left == kLeftTail) mbar_wait(&bars->v_tail, 0, drain_ctx);
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+      for (int t = 0; t < 2; ++t)  // (the queries are copied in any case)
+        if (bars->steps[t] > 0) mbar_wait(&bars->q_full[t], 0, drain_ctx);
+      const int mine_k = bars->k_loads, k = pair_peer_word(&bars->k_loads, 0), nk = max(mine_k, k);
+      for (int j = max(0, nk - kStages); j < nk; ++j)
+        pair_close(&bars->k_full[j % kStages], j / kStages, mine_k > j, k > j, kKStage, false, drain_ctx);
+      const int mine_v = bars->v_loads, v = pair_peer_word(&bars->v_loads, 0), nv = max(mine_v, v);
+      for (int j = max(0, nv - kStages); j < nv; ++j)
+        pair_close(&bars->v_full[j % kStages], j / kStages, mine_v > j, v > j, kVStage, true, drain_ctx);
+    }
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 1000000) {
     }
+    __syncwarp();
   }
   cluster_sync();
   if (warp == 9) {

@@ -60,6 +60,7 @@ struct Params {
   float* lse;
   unsigned int* status;
   uint64_t wait_ns;
+  int stall;  // see host_stall
 };
 
 struct Bars {

@@ -99,18 +99,26 @@ struct WaitCtx {
   uint64_t limit_ns;           // time budget for one wait
 };
 
-template <bool kClusterAcquire = false>
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+struct Nothing {
+  __device__ void operator()() const {}
+};
+template <bool kClusterAcquire = false, class Failed = Nothing>
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w,
+                                          Failed failed = Failed()) {
   const uint32_t a = smem_u32(bar);
   if (kClusterAcquire ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
     if (kClusterAcquire ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
     if ((i & 63) == 0) {
-      if (*w.abort_flag) return false;
+      if (*w.abort_flag) {
+        failed();
+        return false;
+      }
       if (globaltimer_ns() - t0 > w.limit_ns) {
         *w.abort_flag = 1;
         atomicOr(w.status, MLA_STATUS_TIMEOUT);
+        failed();
         return false;
       }
     }
@@ -123,6 +131,20 @@ template <bool kClusterAcquire = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
   const bool ok = mbar_wait<kClusterAcquire>(bar, parity, w);
   return __all_sync(0xffffffffu, ok);
+}
+
+// The same; a wait that runs out leaves `value` in shared memory.
+__device__ __forceinline__ bool warp_wait_noted(uint64_t* bar, uint32_t parity, const WaitCtx& w,
+                                                int* note, int value) {
+  const bool ok = mbar_wait(bar, parity, w, [=]() { *note = value; });
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Whether this warp is the one that a test stalls (it first waits on a barrier nothing arrives on):
+// warp n - 1 of every CTA for n = 1 ... 99, with 100 more of the first CTA of each pair alone, with 200
+// more of the second alone.
+__device__ __forceinline__ bool stall_here(int stall, int warp, int rank) {
+  return stall % 100 == warp + 1 && (stall < 100 || stall / 100 == rank + 1);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -370,6 +392,39 @@ __device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols
 // 5.7 ms instead of 4.0 ms for the attention of 1024 tokens over 16384.)
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Counts bytes on a barrier as landed without a copy.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// After an abort, at the leader, when neither CTA of the pair issues any more: waits for the copies
+// of the last phase of its barrier (none if negative) that either its own CTA (`mine`) or the other one
+// (`others`) has issued copies of, `bytes` each.  Where only one has, the phase would never end: the
+// other's arrival or bytes are made up for, so that it ends when the copies that were issued have landed.
+// `each_arrives`: both CTAs announce their own bytes; else the leader announces those of both.
+__device__ __forceinline__ void pair_close(uint64_t* bar, int phase, bool mine, bool others,
+                                           uint32_t bytes, bool each_arrives, const WaitCtx& w) {
+  if (phase < 0) return;
+  if (mine != others) {
+    if (each_arrives)
+      mbar_arrive(bar);
+    else if (mine)
+      mbar_complete_tx(bar, bytes);
+    else
+      mbar_arrive_expect_tx(bar, bytes);
+  }
+  mbar_wait(bar, phase & 1, w);
+}
+// A word of the other CTA's shared memory, at this place in its own.
+__device__ __forceinline__ int pair_peer_word(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(v)
+               : "r"(mapa_shared(smem_u32(p), rank ^ 1u))
+               : "memory");
+  return v;
 }
 // Announces bytes to come; says nothing of what was done before.
 __device__ __forceinline__ void arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
