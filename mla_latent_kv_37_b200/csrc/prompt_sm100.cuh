@@ -74,11 +74,17 @@ struct Bars {
   uint64_t p_full[2];         // the same: all of P written (4)
   uint64_t o_full[2];         // MMA: the tile's last PV is done (commit)
   uint64_t drain;
+  uint64_t stall;             // nothing ever arrives here (test of a wait that runs out)
   uint32_t tmem_base;
   int steps[2], len;          // key tiles of the two query tiles, tokens: for the MMA issuer
   int abort_flag;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// (a call: inlined, the wait costs six packed prompts of 8192 tokens 1167 instead of 1115 us)
+static __device__ __noinline__ void stall_warp(uint64_t* bar, const WaitCtx& w) {
+  (void)warp_wait(bar, 0, w);
+}
 
 // 168 registers: three of the ten warps share a sub-partition's 16384
 __global__ void __maxnreg__(168)
@@ -120,6 +126,7 @@ __global__ void __maxnreg__(168)
       mbar_init(&bars->v_empty[i], 1);
     }
     mbar_init(&bars->drain, 1);
+    mbar_init(&bars->stall, 1);
     bars->abort_flag = 0;
     bars->steps[0] = n0;
     bars->steps[1] = n1;
@@ -137,6 +144,7 @@ __global__ void __maxnreg__(168)
   const WaitCtx wc{&bars->abort_flag, p.status, p.wait_ns};
   volatile int never = 0;
   const WaitCtx drain_ctx{&never, p.status, kDrainNs};
+  if (p.stall != 0 && stall_here(p.stall, warp, 0)) stall_warp(&bars->stall, wc);
 
   if (warp == 8) {
     // =================== TMA producer ===================

@@ -100,3 +100,9 @@ def test_prompt_pair_waits_that_run_out(monkeypatch, tokens):
     # (rows behind the last sequence make it 2048 tokens, for which pairs are taken)
     p = Prompt(82, tokens, 16, 4, torch.bfloat16, extra=2048 - sum(tokens))
     _check_stalls(_prompt(p), monkeypatch, PAIR_STALLS)
+
+
+# warps 0 ... 7 softmax (four a tile), 8 producer, 9 issuer
+@pytest.mark.parametrize("tokens", [[1], [130], [300, 70, 1000]])
+def test_prompt_waits_that_run_out(monkeypatch, tokens):
+    _check_stalls(_prompt(Prompt(83, tokens, 16, 4, torch.bfloat16)), monkeypatch, [1, 4, 5, 8, 9, 10])
