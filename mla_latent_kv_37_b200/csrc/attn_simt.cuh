@@ -360,11 +360,10 @@ __global__ void __launch_bounds__(PromptLayout::kThreads, 2) prompt_kernel(const
   griddep_wait();
   int seq, index, count;
   packed::Span s;
-  bool bad = false;
   const int h = blockIdx.x % p.n_heads, hk = h / (p.n_heads / p.n_kv_heads);
   const bool there = packed::warp_find_tile(p.cu, p.batch, p.n_tokens, kRows,
-                                            blockIdx.x / p.n_heads, seq, index, count, s, &bad);
-  if (bad && blockIdx.x == 0) atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
+                                            blockIdx.x / p.n_heads, seq, index, count, s);
+  if (blockIdx.x == 0) packed::check_offsets(p.cu, p.batch, p.n_tokens, p.status);
   if (!there) return;
   const int first = (count - 1 - index) * kRows, rows = min(kRows, s.size() - first);
   const int64_t t0 = s.begin;

@@ -24,6 +24,16 @@ __device__ __forceinline__ Span span(const int32_t* cu, int b, int n_tokens, boo
   return {s0, s1};
 }
 
+// Reports offsets that decrease or pass n_tokens.  All threads of one block of a grid, which looks at all
+// sequences: the others look only as far as their own (right behind that look-up the first of these
+// loads are in L1).
+__device__ __forceinline__ void check_offsets(const int32_t* cu, int B, int n_tokens,
+                                              unsigned int* status) {
+  bool bad = false;
+  for (int b = threadIdx.x; b < B; b += blockDim.x) (void)span(cu, b, n_tokens, &bad);
+  if (bad) atomicOr(status, MLA_STATUS_BAD_LENGTH);
+}
+
 // The sequence of token t: the number of entries cu[1 .. B] that are <= t (B if the token lies
 // behind the last sequence).  A 32-way search by one warp: ceil(log32 B) dependent reads.
 __device__ __forceinline__ int warp_sequence_of(const int32_t* cu, int B, int t) {
@@ -48,11 +58,11 @@ __device__ __forceinline__ int warp_sequence_of(const int32_t* cu, int B, int t)
 // Within a sequence the caller may number its tiles in either direction.
 __device__ __forceinline__ bool warp_find_tile(const int32_t* cu, int B, int n_tokens,
                                                int tile_rows, int tile, int& seq, int& index,
-                                               int& count, Span& s, bool* bad) {
+                                               int& count, Span& s) {
   const int lane = threadIdx.x & 31;
   for (int b0 = 0; b0 < B; b0 += 32) {
     Span mine{0, 0};
-    if (b0 + lane < B) mine = span(cu, b0 + lane, n_tokens, bad);
+    if (b0 + lane < B) mine = span(cu, b0 + lane, n_tokens);
     const int n = (mine.size() + tile_rows - 1) / tile_rows;
     int x = n;
 #pragma unroll

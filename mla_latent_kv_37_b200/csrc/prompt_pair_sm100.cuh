@@ -75,10 +75,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
   griddep_wait();
   int seq, index, count;
   packed::Span sp;
-  bool bad = false;
   const bool there = packed::warp_find_tile(p.cu, p.batch, p.n_tokens, kRows, blockIdx.x >> 1, seq,
-                                            index, count, sp, &bad);
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
+                                            index, count, sp);
+  if (blockIdx.x == 0 && blockIdx.y == 0) packed::check_offsets(p.cu, p.batch, p.n_tokens, p.status);
   if (!there) return;  // the whole pair
   // the sequence's last rows first: they have the most keys
   const int q0 = (count - 1 - index) * kRows, len = sp.size();

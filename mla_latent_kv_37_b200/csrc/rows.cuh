@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
       }
     }
     if (lane == 0) slot[warp] = s;
+    if (blockIdx.x == 0) packed::check_offsets(p.cu, p.batch, p.n_tokens, p.status);
   }
   __syncthreads();
   if (rows) {
