@@ -120,7 +120,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
   const WaitCtx wc{&bars->abort_flag, p.status, p.wait_ns};
   volatile int never = 0;
   const WaitCtx drain_ctx{&never, p.status, kDrainNs};
-  if (p.stall != 0 && stall_here(p.stall, warp, rank)) (void)warp_wait(&bars->stall, 0, wc);
+  if (p.stall != 0) {
+    if (stall_here(p.stall, warp, rank)) prompt::stall_warp(&bars->stall, wc);
+    __syncwarp();
+  }
 
   if (warp == 8) {
     // =================== TMA producer: this CTA's rows, keys and columns ===================
