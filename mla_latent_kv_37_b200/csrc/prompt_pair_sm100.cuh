@@ -35,6 +35,7 @@ constexpr uint32_t kOffBar = kOffV + kStages * kVStage;
 constexpr uint32_t kSmemBytes = kOffBar + 512;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 using prompt::kDrainNs;
+using prompt::kLowest;
 using prompt::kRescaleThreshold;
 using prompt::kTmemCols;
 using prompt::kTmemO;
@@ -291,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
       float alpha = 1.f;
       bool move = false;
       if (j == 0) {
-        m_ref = m == NEG_INF ? 0.f : m;
+        m_ref = fmaxf(m, kLowest);
       } else if (m > m_ref + kRescaleThreshold) {
         alpha = ex2_approx(m_ref - m);
         m_ref = m;

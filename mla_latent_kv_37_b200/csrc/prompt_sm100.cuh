@@ -50,6 +50,9 @@ constexpr uint32_t kSmemBytes = kOffBar + 512;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// The reference of a row whose scores so far are all -inf (no key seen, or products beyond fp32): every
+// weight is 0 under it, and any score that is finite moves it.
+constexpr float kLowest = -3.402823466e38f;
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct Params {
@@ -304,7 +307,7 @@ __global__ void __maxnreg__(168)
       float alpha = 1.f;
       bool move = false;
       if (j == 0) {
-        m_ref = m == NEG_INF ? 0.f : m;
+        m_ref = fmaxf(m, kLowest);
       } else if (m > m_ref + kRescaleThreshold) {
         alpha = ex2_approx(m_ref - m);
         m_ref = m;
