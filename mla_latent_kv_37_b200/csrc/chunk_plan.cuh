@@ -50,8 +50,9 @@ struct Tile {
   __device__ int visible(int r, int n_heads) const {
     return min(max(first + (row0 + r) / n_heads + 1, 0), len);
   }
-  __device__ int blocks(const Shape& s) const {
-    return (visible(rows - 1, s.n_heads) + (1 << s.block_shift) - 1) >> s.block_shift;
+  __device__ int blocks(const Shape& s) const {  // (the sum may pass 2^31, by less than a block)
+    return static_cast<int>(
+        (static_cast<unsigned>(visible(rows - 1, s.n_heads)) + (1u << s.block_shift) - 1) >> s.block_shift);
   }
 };
 // Tiles of a sequence, and its k-th one.

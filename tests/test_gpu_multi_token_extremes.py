@@ -148,3 +148,25 @@ def test_chunk_rising_maxima(dtype, tokens, lens, splits):
     o, l, st = c.run(splits)
     assert st == 0
     _check_chunk(c, o, l, 1100 * SCALE / math.log(2))
+
+
+def test_chunk_longest_sequence():
+    """The most rows that a page table may name, 2^31 - 64, all on one page: the page's own softmax, with a
+    sum (2^31 - 64) / 64 times its own.  A part adds up to 2^31 / 24 / 128 blocks' sums one behind the other,
+    each with a rounding of 2^-24 of the sum at most, all to one side: 4.2% of it."""
+    import mla_latent_kv_37_b200 as M
+    from tests.gpu_common import dev
+    pages = (1 << 25) - 1
+    g = I.generator(111)
+    q, row = torch.randn(1, 16, 576, generator=g).bfloat16(), torch.randn(64, 576, generator=g).bfloat16()
+    o = torch.empty(1, 16, 512, dtype=torch.bfloat16, device="cuda")
+    l = torch.empty(1, 16, device="cuda")
+    d = M.dims(1, 16)
+    M.mla_chunk_attn(d, dev(q), dev(row)[None], torch.zeros(1, pages, dtype=torch.int32, device="cuda"),
+                     dev(_cu([1])), dev(torch.tensor([64 * pages], dtype=torch.int32)), o,
+                     M.chunk_workspace(d, 1), lse=l)
+    assert M.mla_get_status() == 0
+    r = O.f64(row)
+    _, lse = O.latent_attention(O.f64(q[0])[:, :512], O.f64(q[0])[:, 512:], r[:, :512], r[:, 512:])
+    np.testing.assert_allclose(to_np(l[0].cpu()), lse + math.log(pages), rtol=0, atol=0.042 + 1e-3)
+    assert torch.isfinite(o).all()
