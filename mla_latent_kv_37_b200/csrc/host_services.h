@@ -26,7 +26,7 @@ bool host_pdl();
 uint64_t host_wait_ns();
 // MLA_TEST_STALL of the environment, read at each call: 0 unless it is a number from 1 to 299.
 int host_stall();
-// The checks of mla_dims that do not limit the batch.
+// The checks of mla_dims that neither limit the batch nor look at d_model.
 int host_check_dims(const mla_dims* d);
 int host_encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank,
                 const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,

@@ -70,14 +70,14 @@ constexpr size_t kSmemPerBlockMax = 232448;  // 227 KiB opt-in limit per CTA
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // `one_token`: the calls that take one token per sequence, whose bf16 products put the batch on
-// the MMA's columns.
+// the MMA's columns.  The others have no use for d_model.
 int check_dims(const mla_dims* d, bool one_token = true) {
   if (!d) return MLA_ERR_NULL_ARG;
   if (d->d_c != kDc || d->d_rope != kDr || d->d_nope != kDn || d->d_v != kDv ||
       d->page_size != kPageN)
     return MLA_ERR_DIMS;
   if (d->n_heads < 16 || d->n_heads > 128 || d->n_heads % 16) return MLA_ERR_DIMS;
-  if (d->d_model <= 0 || d->d_model % 64) return MLA_ERR_DIMS;
+  if (one_token && (d->d_model <= 0 || d->d_model % 64)) return MLA_ERR_DIMS;
   if (d->batch < 1) return MLA_ERR_DIMS;
   if (d->dtype != MLA_BF16 && d->dtype != MLA_FP32) return MLA_ERR_DIMS;
   if (one_token && d->dtype == MLA_BF16 && d->batch > 128) return MLA_ERR_DIMS;  // 2B <= 256 MMA columns
