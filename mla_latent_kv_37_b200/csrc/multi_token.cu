@@ -18,10 +18,11 @@ namespace {
 
 constexpr int kDc = 512, kDr = 64, kDn = 128, kDv = 128, kPageN = 64;
 constexpr int kMaxParts = 1 << 16;
-// Prompts of this many tokens on average run on pairs of SMs (64 heads, 8192 tokens in all: 4096 each
-// 719 us on pairs, 756 us without; 2048 each 442 and 440 us, and one of 2048 alone 139 and 147 us;
-// 1024 each 329 and 289 us, 256 each 340 and 179 us, since a pair's 512 rows fill badly).
-constexpr int kPairTokens = 2048;
+// Prompts of this many tokens on average run on pairs of SMs (one of 16384, 32 heads: 2.37 ... 2.41 ms on
+// pairs, 2.48 ... 2.51 ms without; 64 heads, 8192 tokens in all: 4096 each 687 ... 737 us and 696 ... 714 us;
+// 2048 each 454 ... 463 and 428 us, and one of 2048 alone 134 ... 137 and 129 ... 132 us; 1024 each 333 ...
+// 337 and 278 us, 256 each 346 and 178 us, since a pair's 512 rows fill badly).
+constexpr int kPairTokens = 4096;
 constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -48,7 +48,7 @@ def test_prompt_offsets(dtype, B):
 
 def test_prompt_offsets_on_pairs():
     import mla_latent_kv_37_b200 as M
-    B, T = 40, 40 * 2048  # (pairs are taken from 2048 tokens a sequence on; most lie behind the last one)
+    B, T = 40, 40 * 4096  # (pairs are taken from 4096 tokens a sequence on; most lie behind the last one)
     d = M.dims(B, 16)
     q, k, kr = (torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
                 for s in ((T, 16, 192), (T, 1, 128), (T, 64)))

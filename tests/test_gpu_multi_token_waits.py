@@ -97,8 +97,8 @@ PAIR_STALLS = [1, 104, 203, 5, 208, 9, 109, 209, 10, 11, 110]
 
 @pytest.mark.parametrize("tokens", [[2011], [1920], [130], [17]])
 def test_prompt_pair_waits_that_run_out(monkeypatch, tokens):
-    # (rows behind the last sequence make it 2048 tokens, for which pairs are taken)
-    p = Prompt(82, tokens, 16, 4, torch.bfloat16, extra=2048 - sum(tokens))
+    # (rows behind the last sequence make it 4096 tokens, for which pairs are taken)
+    p = Prompt(82, tokens, 16, 4, torch.bfloat16, extra=4096 - sum(tokens))
     _check_stalls(_prompt(p), monkeypatch, PAIR_STALLS)
 
 
