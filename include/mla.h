@@ -94,7 +94,8 @@ typedef struct mla_dims {
 
 /* Device-detected conditions (bits of the status word, see mla_get_status). */
 #define MLA_STATUS_BAD_PAGE 0x1u     /* a page id outside [0, num_pages) was skipped */
-#define MLA_STATUS_BAD_LENGTH 0x2u   /* a sequence length outside [0, max_pages*page_size] */
+#define MLA_STATUS_BAD_LENGTH 0x2u   /* a sequence length outside [0, max_pages*page_size], or
+                                        cu_tokens that decrease or pass n_tokens */
 #define MLA_STATUS_TIMEOUT 0x4u      /* a bounded wait inside a kernel gave up */
 #define MLA_STATUS_BAD_POSITION 0x8u /* an append position outside the sequence's pages */
 
@@ -308,13 +309,16 @@ int mla_out_proj_fp8(const mla_dims* dims, const float* o_lat, const void* w_uv,
  * tokens [cu_tokens[b], cu_tokens[b + 1]) of n_tokens, cu_tokens [batch + 1] int32 on the device,
  * cu_tokens[0] = 0, not decreasing, cu_tokens[batch] <= n_tokens.  A sequence may have none.
  * Tokens behind the last sequence have no influence and are not written.  A cu_tokens that decreases or
- * passes n_tokens raises MLA_STATUS_BAD_LENGTH and gives undefined results for the sequences it
- * damages, without an access out of range.
+ * passes n_tokens raises MLA_STATUS_BAD_LENGTH, wherever it does, and gives undefined results for the
+ * sequences it damages, without an access out of range.
  * seq_lens[b] counts the sequence's rows with its new tokens: token i of n_b is row
  * seq_lens[b] - n_b + i.  dims.batch is the number of sequences; in these calls it is not limited
- * to 128, and d_model is not used.  n_tokens = 0 does nothing.
- * Strides are in elements, at least the row they step over and at most 2^36, and multiples of 16
+ * to 128 (though every block of mla_prompt_attn looks its sequence up among all, 32 at a time), and
+ * d_model is not used.  n_tokens = 0 does nothing.
+ * Strides are in elements, at least the row they step over and less than 2^36, and multiples of 16
  * bytes (else MLA_ERR_ARG), so a view of a wider tensor can be passed as it is.
+ * Outputs may overlap neither inputs nor one another, but where a call says so.  That is not checked:
+ * such a call stays in bounds, and its values are undefined.
  *
  * mla_append_rows -- the rows of the new tokens into the cache, the rotation applied on the way:
  *   pool slot of row p = seq_lens[b] - n_b + i:  [c_kv[t] | R(p) k_r[t]],
@@ -323,7 +327,10 @@ int mla_out_proj_fp8(const mla_dims* dims, const float* o_lat, const void* w_uv,
  *   c_kv [n_tokens, d_c], k_r [n_tokens, d_rope], rows c_kv_stride / k_r_stride apart.
  *   k_rope   nullable: [n_tokens, d_rope] contiguous (for mla_prompt_attn).
  *   q_rope, q_rope_out  nullable together: [n_tokens, H, d_rope]; q_rope_out may be q_rope (in
- *            place), or the last d_rope columns of q_cat, but may not overlap it otherwise.
+ *            place: the same address and strides).  It may be a view, such as the last d_rope
+ *            columns of q_cat, whose rows do not overlap.
+ * A row is mla_cache_append's but for the last bits of the rotation: the frequencies are 2^x here and
+ * a power there, in 64 bits.
  * A token whose row lies outside its sequence's pages (MLA_STATUS_BAD_POSITION) or whose page id
  * is out of range (MLA_STATUS_BAD_PAGE) is skipped: nothing of it is written.  Two tokens may not
  * share a slot.
@@ -350,7 +357,8 @@ int mla_append_rows(const mla_dims* dims, int32_t n_tokens, const int32_t* cu_to
  *   softmax_scale: 0 selects 1/sqrt(d_nope + d_rope).
  * No workspace.  The rows of one sequence never depend on another's, nor on what lies behind the
  * last one.  Within a sequence, v has to be finite (a later token's value has weight zero, which
- * does not silence a NaN); a NaN in q or k shows in the rows that see it and in no other.
+ * does not silence a NaN); a NaN in q or k shows in the rows that see it and in no other.  On the
+ * bf16 path the weights softmax(s) are rounded to bf16 before they meet v; their sum is not.
  */
 int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
                     const int32_t* cu_tokens, const void* q, int64_t q_token_stride,
@@ -369,6 +377,10 @@ int mla_prompt_attn(const mla_dims* dims, int32_t n_tokens, int32_t n_kv_heads,
  *   o_lat  [n_tokens, H, d_c] of type o_dtype: dims.dtype, or MLA_FP32 (for mla_out_proj and
  *          mla_merge_partials); on the bf16 path the weights p are rounded to bf16 either way.
  *   lse    [n_tokens, H] fp32, nullable.
+ * Unlike mla_decode_attn the call takes no q_lo: where logits are large, a bf16 query's rounding
+ * shows here and not there.  And a token's last visible row is counted from the end of seq_lens, so a
+ * rank that holds only a sequence's beginning can let one new token see all of it (n_b = 1), not
+ * several; partial results of several ranks are for one token per sequence.
  * What the pool holds behind a sequence's last row has no influence, whatever it is (NaN too); the
  * sequence's own rows have to be finite.
  * A token that sees no row (n_b > seq_lens[b]) gets o_lat = 0, lse = -inf.  Lengths outside

@@ -12,12 +12,14 @@
 // O += P V in slices of keys with O in registers (8 rows x DV / 32 columns a thread).  The slices,
 // 16 KB each, come by cp.async two steps ahead through three stages, with one block barrier a step.
 //
-// Bound by the FMA pipe, 2 (DQ + DV) flops per row and key at 128 FMAs a clock and SM, and more by
-// the loads from shared memory: one of 16 bytes takes about four clocks of the SM, whether or not
-// the lanes read the same address, so 64 FMAs (16 clocks of the SM) that follow 8 loads (4 rows x
-// 4 keys a thread) take 32.  (2 x 8 and 8 x 2 follow 10; a slice of 64 rows x 64 keys measured
-// 4450 clocks with them.)  Prompts of 500, 129 and 33 tokens, 16 heads: 97 us (14 TFLOP/s); 33 and 7
-// tokens over 700 and 129 rows: 47 us and the merge.
+// The work is 2 (DQ + DV) flops per row and key at 128 FMAs a clock and SM, and the loads from shared
+// memory take twice that: one of 16 bytes costs about four clocks of the SM, whether or not the lanes
+// read the same address, so 64 FMAs (16 clocks of the SM) that follow 8 loads (4 rows x 4 keys a
+// thread) take 32.  (2 x 8 and 8 x 2 follow 10; a slice of 64 rows x 64 keys measured 4450 clocks with
+// them.)  Small calls are bound by neither (FMA and shared memory are both busy for 30 ... 40% of the
+// clocks in the two below) but by one tile's chain: a block walks over the tile's keys alone, a barrier
+// a slice, with two to four warps a scheduler.  Prompts of 500, 129 and 33 tokens, 16 heads: 98 us (14
+// TFLOP/s); 33 and 7 tokens over 700 and 129 rows: 48 us with the merge.
 #pragma once
 #include "chunk_plan.cuh"
 
@@ -431,7 +433,8 @@ constexpr int kChunkBlock = 1 << kChunkBlockShift;
 using ChunkLayout = Layout<576, 512, kChunkWarps, 1>;
 static_assert(ChunkLayout::kRows == 1 << kChunkTileShift, "a tile's rows");
 // Costs in quarters of a block of 16 keys: a segment's start and write-back take the time of about
-// two blocks (40 tokens of 16 heads over 829 rows: 61 us; 79 us with half a block for them).
+// two blocks (40 tokens of 16 heads over 829 rows: 49 ... 58 us; 65 ... 71 us with half a block for them,
+// 55 ... 59 us with four; eight single tokens, and one over 4096 rows: the same with each).
 constexpr int kChunkCostShift = 2, kChunkSegCost = 8, kChunkLeast = 4;
 
 __global__ void __launch_bounds__(ChunkLayout::kThreads, 1) chunk_kernel(const ChunkParams p) {

@@ -28,8 +28,9 @@
 // Bound by the tensor pipe, 2176 flops per visible pair of row and key, and behind it by the power
 // limit: 1024 tokens over 16384 rows, 128 heads 3.3 ... 3.7 ms, 1.23 ... 1.37 PFLOP/s (a library
 // matrix product runs at 1.37 for seconds on end).  32 x 4 tokens over 4096 ... 8126 rows: 185 ...
-// 225 us.  Eight single tokens: 24 us, of which the first copies' latency, the partial results and
-// their merge are the most.
+// 225 us, the pipe at 60%: a ring holds one block, so that a page that comes from HBM holds the products
+// up, and the merge (15 us) follows.  Eight single tokens: 24 us, of which the first copies' latency, the
+// partial results and their merge are the most.
 #pragma once
 #include "chunk_plan.cuh"
 
@@ -39,7 +40,9 @@ namespace chunk {
 constexpr int kTileShift = 7, kTileRows = 1 << kTileShift, kCtaRows = 64;
 constexpr int kBlockShift = 7, kBlock = 1 << kBlockShift;  // keys per block: two pages
 // Costs in blocks: a segment's start and write-back take the time of about four.  Parts of at least
-// four: eight single tokens over 64 ... 3000 keys take 25 us, 27 us with parts of two.
+// four; with parts of two, and of eight and a cost of eight, 128 heads: eight single tokens over 1 ...
+// 3000 keys 25.4 us (27.5, 29.7), one over 700 22.4 (19.2, 22.1), one over 16384 36.9 (36.9, 33.9), 32 x 4
+// over 4096 ... 8126 186 (186, 189); 16 heads: 64 single tokens over 500 27.5 (27.5, 27.0).
 constexpr int kCostShift = 0, kSegCost = 4, kLeast = 4;
 constexpr int kThreads = 256;  // 4 softmax warps, key producer, S issuer, value producer, O issuer
 constexpr uint32_t kBoxBytes = 64 * 128;  // 64 rows x 64 bf16

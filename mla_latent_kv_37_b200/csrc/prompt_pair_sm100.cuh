@@ -7,8 +7,8 @@
 // for 128 keys where a CTA of its own moves 80 KB, and its tensor core reads 6 KB instead of 8 KB of
 // shared memory for a 128 x 128 x 16 product.  At full load the GPU runs at its power limit, so that
 // this is what the rate depends on.
-// One prompt of 16384 tokens, 32 query and 4 key heads: 2.23 ... 2.44 ms, 1.13 ... 1.23 PFLOP/s, where
-// CTAs of their own take 2.50 ... 2.66 ms.
+// One prompt of 16384 tokens, 32 query and 4 key heads: 2.36 ... 2.47 ms, 1.11 ... 1.16 PFLOP/s, where
+// CTAs of their own take 2.48 ... 2.51 ms on the box of 2.37 ... 2.41.
 // Softmax and tensor memory are those of prompt_sm100.cuh; the leader (CTA 0) issues for both, so
 // barriers that it waits on collect both CTAs' arrivals.  A tile's products are issued by a warp of
 // its own, in the order PV(j) S(j+1): neither tile's waits hold up the other (2.32 ms with one

@@ -21,10 +21,12 @@
 // the last 16 keys that hold one of the sequence, and the values of the others among those 16 are
 // set to zero first, since a weight of zero does not silence a NaN.
 //
-// Bound by the tensor pipe, 640 flops per visible pair of rows and head, and behind it by the power
-// limit (1 kW, 1.7 GHz instead of 1.9).  8192 tokens in six prompts, 128 heads: 1.06 ... 1.18 ms,
-// 0.82 ... 0.87 PFLOP/s.  Two tiles fill 53% of the pipe's clocks: a tile's softmax (2100 clocks) and
-// its products (1280) follow one another, since P lies over S.  What was tried against that: P in
+// The work is 640 flops per visible pair of rows and head.  8192 tokens in six prompts, 128 heads:
+// 1.11 ... 1.15 ms, 0.81 ... 0.83 PFLOP/s, at 1.7 GHz (the power limit, 1 kW).  The tensor pipe is not
+// full: 32% of its clocks with prompts of 2048 and 1000 tokens, 64 heads.  A tile's softmax (2100 clocks)
+// and its products (1280) follow one another, since S(j+1) is written over all of S after PV(j) has read
+// P from its first half; and a block's start and end (search, barriers, tensor memory, first copies,
+// write-back) overlap with nothing, one block to an SM.  What was tried against the first: P in
 // shared memory, so that S(j+1) need not wait for PV(j) (3.4 ms instead of 2.6 ms for one prompt of
 // 16384: the ring shrinks to four boxes, and both operands of PV come from shared memory); an order
 // between the two tiles' exponentials (2.64); a part of the exponentials as a polynomial on the FMA
