@@ -357,9 +357,9 @@ struct Split {
 // columns 4 (l + 32 k) ... + 3.
 template <typename O>
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_rows_kernel(int parts, int tile_rows, const PartStart* __restrict__ starts,
-                        const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                        O* __restrict__ o, float* __restrict__ lse) {
+    combine_rows_kernel(int parts, int tile_rows, const PartStart* starts,
+                        const float* part_o, const float* part_lse,
+                        O* o, float* lse) {
   griddep_launch_dependents();
   griddep_wait();
   Split sp;
@@ -407,9 +407,9 @@ __global__ void __launch_bounds__(kCombineThreads)
 // columns 128 z + 4 (w + 8 k) ... + 3, k < 4.  The rows go out through shared memory.
 template <typename O>
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_columns_kernel(int parts, int tile_rows, const PartStart* __restrict__ starts,
-                           const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                           O* __restrict__ o, float* __restrict__ lse) {
+    combine_columns_kernel(int parts, int tile_rows, const PartStart* starts,
+                           const float* part_o, const float* part_lse,
+                           O* o, float* lse) {
   __shared__ float4 turn[32][33];
   griddep_launch_dependents();
   griddep_wait();

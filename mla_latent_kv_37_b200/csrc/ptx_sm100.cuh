@@ -154,7 +154,9 @@ __device__ __forceinline__ bool stall_here(int stall, int warp, int rank) {
 // start while the preceding kernel on its stream is still running: it must call griddep_wait()
 // before it touches anything that kernel writes (or reads), and griddep_launch_dependents()
 // lets the following kernel be scheduled as soon as every CTA of this one has called it.
-// Both are no-ops when the kernel was launched normally.
+// Both are no-ops when the kernel was launched normally.  What the preceding kernel writes is read with
+// ordinary loads: one that the compiler takes for invariant (__ldg, const __restrict__) is bound to no
+// wait, and may be moved in front of it.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

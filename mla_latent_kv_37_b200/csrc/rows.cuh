@@ -87,10 +87,9 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
       const int64_t t = t0 + k;
       if (k < n_here)
         v[u] = c < kLatChunks
-                   ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.c_kv) +
-                                                          t * p.c_stride) + c)
-                   : __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_r) +
-                                                          t * p.kr_stride) + (c - kLatChunks));
+                   ? reinterpret_cast<const uint4*>(static_cast<const T*>(p.c_kv) + t * p.c_stride)[c]
+                   : reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_r) +
+                                                    t * p.kr_stride)[c - kLatChunks];
     }
   } else if (h < p.n_heads) {
     const T* src = static_cast<const T*>(p.q) + t0 * p.q_tok + h * p.q_head + r * kN;
