@@ -195,8 +195,8 @@ __device__ inline int part_of_page(int64_t v, int C, int64_t V) {
 // whose first page lies inside sequence b are written by b's thread, so no thread searches the
 // prefix sums that other threads wrote.
 __global__ void __launch_bounds__(kPlanThreads)
-    plan_kernel(const int32_t* __restrict__ seq_lens, int B, int max_pages, int C_req,
-                int min_pages_per_part, int32_t* __restrict__ plan, unsigned int* status) {
+    plan_kernel(const int32_t* seq_lens, int B, int max_pages, int C_req,
+                int min_pages_per_part, int32_t* plan, unsigned int* status) {
   griddep_launch_dependents();
   griddep_wait();
   __shared__ int warp_sums[32];
@@ -742,7 +742,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
         uint4 v[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          v[k] = in ? __ldg(src + 16 * half + k) : make_uint4(0u, 0u, 0u, 0u);
+          v[k] = in ? src[16 * half + k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t r[32];
@@ -984,9 +984,9 @@ constexpr int kCombineWarps = 8;
 // One warp per (sequence, head); lane l owns float4 columns l, l + 32, l + 64 and l + 96.  The
 // parts are merged in slot order; every part's loads of a chunk are issued before any is used.
 __global__ void __launch_bounds__(32 * kCombineWarps)
-    combine_kernel(const int32_t* __restrict__ plan_words, int B, int C, int H,
-                   const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                   float* __restrict__ o_lat, float* __restrict__ lse) {
+    combine_kernel(const int32_t* plan_words, int B, int C, int H,
+                   const float* part_o, const float* part_lse,
+                   float* o_lat, float* lse) {
   griddep_launch_dependents();
   griddep_wait();
   const PlanView plan(plan_words, B, C);
@@ -1049,9 +1049,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
 // weighs nothing; a row whose parts are all empty gets o = 0, lse = -inf.
 // ------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(32 * kCombineWarps)
-    merge_kernel(int n, int rows, const float* __restrict__ part_o,
-                 const float* __restrict__ part_lse, float* __restrict__ o_lat,
-                 float* __restrict__ lse) {
+    merge_kernel(int n, int rows, const float* part_o,
+                 const float* part_lse, float* o_lat,
+                 float* lse) {
   griddep_launch_dependents();
   griddep_wait();
   const int row = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);

@@ -149,8 +149,8 @@ __global__ void wuk_epilogue_kernel(const float* __restrict__ part, int n_pad, i
 // plane are multiples of 8 and x, out 16-byte aligned: each thread converts 8 values with one
 // 32-byte load and two 16-byte stores.  Also zeroes zero[0 .. n_zero) (block 0), a buffer the
 // next kernel accumulates into.
-__global__ void split_hi_lo_kernel(const float* __restrict__ x, size_t n, size_t plane,
-                                   __nv_bfloat16* __restrict__ out, unsigned int* zero,
+__global__ void split_hi_lo_kernel(const float* x, size_t n, size_t plane,
+                                   __nv_bfloat16* out, unsigned int* zero,
                                    int n_zero) {
   griddep_launch_dependents();
   griddep_wait();

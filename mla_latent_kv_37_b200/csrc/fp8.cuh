@@ -67,9 +67,9 @@ __device__ __forceinline__ float2 e4m3x2_value(uint16_t c) {
 // [n_planes][rows_pad][K]; rows in [rows, rows_pad) are written as zeros.  Each thread converts
 // 8 consecutive values (grid-stride); K a multiple of 8; x and planes 16- and 8-byte aligned.
 __global__ void __launch_bounds__(256)
-    split_planes_kernel(const float* __restrict__ x, const unsigned int* __restrict__ rowmax,
+    split_planes_kernel(const float* x, const unsigned int* rowmax,
                         int rows, long long K, int rows_pad, int n_planes,
-                        uint8_t* __restrict__ planes, float* __restrict__ scale) {
+                        uint8_t* planes, float* scale) {
   griddep_launch_dependents();
   griddep_wait();
   const long long n8 = K / 8;
@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(256)
 // row's maximum itself (K bf16 values, from L2), then converts its slice of K / slices values,
 // 8 per thread.  K a multiple of 8 * slices; x 16-byte and planes 8-byte aligned.
 __global__ void __launch_bounds__(256)
-    split_planes_bf16_kernel(const __nv_bfloat16* __restrict__ x, int rows, long long K,
-                             int rows_pad, uint8_t* __restrict__ planes,
-                             float* __restrict__ scale) {
+    split_planes_bf16_kernel(const __nv_bfloat16* x, int rows, long long K,
+                             int rows_pad, uint8_t* planes,
+                             float* scale) {
   __shared__ float part[8];
   griddep_launch_dependents();
   griddep_wait();

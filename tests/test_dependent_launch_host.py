@@ -8,7 +8,8 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mla_latent_kv_37_b200", "csrc")
-FILES = ["attn_simt.cuh", "chunk_plan.cuh", "chunk_sm100.cuh", "prompt_pair_sm100.cuh", "prompt_sm100.cuh", "rows.cuh"]
+FILES = ["attn_simt.cuh", "attn_sm100.cuh", "chunk_plan.cuh", "chunk_sm100.cuh", "epilogue.cuh", "fp8.cuh", "gemm_streamk.cuh",
+         "prompt_pair_sm100.cuh", "prompt_sm100.cuh", "rows.cuh"]
 
 
 @pytest.mark.parametrize("name", FILES)
