@@ -14,7 +14,7 @@
 // from HBM once.  With ranges of one list of tiles they read them at w different times, and 32 x 4
 // tokens over 225 MB of rows read 779 MB.  Not for caches that stay in L2 anyway, nor where the
 // parts are not nearly a multiple of w.  One sequence with another number of tiles turns teams off for
-// all: 31 x 4 tokens and one of 5 take 247 us, 32 x 4 take 211.
+// all: 31 x 4 tokens and one of 5 take 207 ... 248 us, 32 x 4 take 193 ... 211.
 //
 // Every block of the attention kernel finds its own range, a tile a thread and two passes where the
 // tiles are more than the threads: a kernel of its own for the plan took 6 us before the first load.
